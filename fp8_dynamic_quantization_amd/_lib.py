@@ -25,6 +25,11 @@ HQ_PER_CHANNEL = 2
 HQ_BIAS_BF16 = 0
 HQ_BIAS_E4M3 = 1
 HQ_BIAS_E5M2 = 2
+HQ_ACT_NONE = 0
+HQ_ACT_RELU = 1
+HQ_ACT_GELU = 2
+HQ_ACT_GELU_TANH = 3
+HQ_ACT_SILU = 4
 
 
 class hq_ring(ctypes.Structure):
@@ -40,6 +45,14 @@ class hq_ring(ctypes.Structure):
 class hq_epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32), ("bias_scale", ctypes.c_void_p),
                 ("out_scale", ctypes.c_void_p), ("out_fmt", ctypes.c_int32)]
+
+
+class hq_fused_epilogue(ctypes.Structure):
+    _fields_ = hq_epilogue._fields_ + [("act", ctypes.c_int32), ("residual", ctypes.c_void_p)]
+
+
+class hq_checkpoint(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block_size", ctypes.c_int32)]
 
 
 class HQError(RuntimeError):
@@ -100,6 +113,17 @@ SIGNATURES = {
     "hq_grouped_gemm_a8w8_strict": (_I, [_P, _I, _P, _I, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64,
                                          ctypes.POINTER(hq_epilogue), _P, _P]),
     "hq_stream_rows_probe": (_I, [_P, _I64, _I64, _I32, _P, _P]),
+    "hq_rmsnorm_quantize_fp8": (_I, [_P, _P, _P, _I, _I64, _I64, ctypes.c_float, _I, _P, _P, _P, _P,
+                                     ctypes.POINTER(hq_checkpoint), _P]),
+    "hq_rmsnorm_backward_workspace_bytes": (_SZ, [_I, _I64, _I64]),
+    "hq_rmsnorm_backward": (_I, [_P, _P, ctypes.POINTER(hq_checkpoint), _P, _P, _P, _I, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "hq_gemm_a8w8_fused": (_I, [_P, _I, _P, _I, _P, _I64, _P, _I64, _I64, _I64, _I64, ctypes.POINTER(hq_fused_epilogue),
+                                _P, _P, _SZ, _P]),
+    "hq_act_quantize_fp8": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _P, _P, ctypes.POINTER(hq_checkpoint), _P]),
+    "hq_act_backward_workspace_bytes": (_SZ, [_I, _I64, _I64, _I]),
+    "hq_act_backward": (_I, [_P, ctypes.POINTER(hq_checkpoint), _I, _I64, _I64, _I, _I, _P, _P, _P, _SZ, _P]),
+    "hq_wgrad_workspace_bytes": (_I64, [_I64, _I64, _I64, _I]),
+    "hq_wgrad_a8": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
     "hq_last_error": (ctypes.c_char_p, []),
 }
 

@@ -13,11 +13,12 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+from typing import NamedTuple
 
 import torch
 
-from ._lib import (HQ_BF16, HQ_BIAS_BF16, HQ_E4M3, HQ_E5M2, HQ_F32, HQ_PER_CHANNEL, HQ_PER_TENSOR,
-                   HQ_PER_TOKEN, check, hq_epilogue, hq_ring, load)
+from ._lib import (HQ_ACT_NONE, HQ_BF16, HQ_BIAS_BF16, HQ_E4M3, HQ_E5M2, HQ_F32, HQ_PER_CHANNEL, HQ_PER_TENSOR,
+                   HQ_PER_TOKEN, check, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_ring, load)
 
 __all__ = [
     "Ring", "hq_scale_count", "hq_quantize_workspace_bytes", "hq_preshuffled_bytes",
@@ -28,6 +29,9 @@ __all__ = [
     "hq_grouped_gemm_a8w8", "hq_grouped_gemm_a8w8_epilogue", "hq_quantize_fp8_preshuffled", "hq_last_error",
     "hq_gemm_a8w8_strict", "hq_grouped_gemm_a8w8_strict", "hq_gemm_a8w8_noalloc",
     "hq_quantize_workspace_status", "hq_stream_rows_probe",
+    "Checkpoint", "RmsNormQuantized", "hq_rmsnorm_quantize_fp8", "hq_rmsnorm_backward_workspace_bytes",
+    "hq_rmsnorm_backward", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward_workspace_bytes",
+    "hq_act_backward", "hq_wgrad_workspace_bytes", "hq_wgrad_a8",
 ]
 
 _XT = {torch.float32: HQ_F32, torch.bfloat16: HQ_BF16}
@@ -536,3 +540,271 @@ def hq_grouped_gemm_a8w8_epilogue(xq: torch.Tensor, xf: int, wq_pre: torch.Tenso
              int(num_experts), t, n, k, ctypes.byref(ep), _ptr(out),
              _stream(xq.device, stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# operators around the GEMM
+# ---------------------------------------------------------------------------
+class Checkpoint(NamedTuple):
+    """An activation kept in 8 bits: E4M3 codes uint8 [rows, cols] and float32
+    scales [rows, ceil(cols / block_size)] (what hq_quantize_fp8_blockwise gives
+    for blocks of 32, 64 or 128)."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    block_size: int
+
+
+class RmsNormQuantized(NamedTuple):
+    """Result of hq_rmsnorm_quantize_fp8; h and checkpoint are None where not asked for."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    h: torch.Tensor | None
+    rstd: torch.Tensor
+    checkpoint: Checkpoint | None
+
+
+def _real2d(x, name):
+    if x.dtype not in _XT:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [rows, cols]")
+    return x.contiguous()
+
+
+def _like(t, shape, dtype, name):
+    """`t` contiguous (None stays None), checked to be of this shape and type."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.contiguous()
+
+
+def _out(t, shape, dtype, device, name):
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _checkpoint_in(c, rows, cols):
+    q = _like(c.q, (rows, cols), torch.uint8, "checkpoint.q")
+    bs = int(c.block_size)
+    s = _like(c.scales, (rows, -(-cols // bs) if bs > 0 else 0), torch.float32, "checkpoint.scales")
+    return Checkpoint(q, s, bs)
+
+
+def _checkpoint_out(c, rows, cols, device):
+    """None or 0: none; a block size: new buffers; a Checkpoint: its buffers."""
+    if c is None or c is False or (isinstance(c, int) and c == 0):
+        return None
+    if isinstance(c, Checkpoint):
+        bs = int(c.block_size)
+        nb = -(-cols // bs) if bs > 0 else 0
+        return Checkpoint(_out(c.q, (rows, cols), torch.uint8, device, "checkpoint.q"),
+                          _out(c.scales, (rows, nb), torch.float32, device, "checkpoint.scales"), bs)
+    bs = int(c)
+    nb = -(-cols // bs) if bs > 0 else 0
+    return Checkpoint(torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                      torch.empty((rows, nb), dtype=torch.float32, device=device), bs)
+
+
+def _checkpoint_c(c):
+    return None if c is None else ctypes.byref(hq_checkpoint(c.q.data_ptr(), c.scales.data_ptr(), c.block_size))
+
+
+_SUM_WORKSPACE = {}
+
+
+def _sum_workspace(device, nbytes):
+    """Scratch for the sums over rows, one per device and stream, kept for
+    reuse. It needs no initial value, and launches on one stream are ordered."""
+    if nbytes <= 0:
+        return None
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    ws = _SUM_WORKSPACE.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _SUM_WORKSPACE[key] = ws
+    return ws
+
+
+@_on_stream
+def hq_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, fmt: int = HQ_E4M3, *,
+                            residual: torch.Tensor | None = None, h=None, checkpoint=None, q=None, scale_out=None,
+                            rstd_out=None, stream=None) -> RmsNormQuantized:
+    """RMS norm of x (+ residual) [rows, cols] times weight [cols] (None: ones),
+    quantized per token. `h`: None (a new buffer when a residual is given), False
+    (not written) or a buffer, which may be x or residual itself. `checkpoint`: a
+    block size or a Checkpoint whose buffers receive h in 8 bits."""
+    x = _real2d(x, "x")
+    rows, cols = x.shape
+    dev, dt = x.device, x.dtype
+    residual = _like(residual, x.shape, dt, "residual")
+    weight = _like(weight, (cols,), dt, "weight")
+    if h is False or (h is None and residual is None):
+        h = None
+    else:
+        h = _out(h, x.shape, dt, dev, "h")
+    q = _out(q, x.shape, torch.uint8, dev, "q")
+    scale_out = _out(scale_out, (rows,), torch.float32, dev, "scale_out")
+    rstd_out = _out(rstd_out, (rows,), torch.float32, dev, "rstd_out")
+    ckpt = _checkpoint_out(checkpoint, rows, cols, dev)
+    check(load().hq_rmsnorm_quantize_fp8(x.data_ptr(), _addr(residual), _addr(weight), _XT[dt], rows, cols, eps, fmt,
+                                         q.data_ptr(), scale_out.data_ptr(), _addr(h), rstd_out.data_ptr(),
+                                         _checkpoint_c(ckpt), _stream(dev, stream)))
+    return RmsNormQuantized(q, scale_out, h, rstd_out, ckpt)
+
+
+def hq_rmsnorm_backward_workspace_bytes(xt: int, rows: int, cols: int) -> int:
+    return int(load().hq_rmsnorm_backward_workspace_bytes(xt, rows, cols))
+
+
+@_on_stream
+def hq_rmsnorm_backward(dy: torch.Tensor, h, weight: torch.Tensor | None, rstd: torch.Tensor, *,
+                        dresidual: torch.Tensor | None = None, dx=None, dweight=None, workspace=None, stream=None):
+    """Backward pass of hq_rmsnorm_quantize_fp8: returns (dx of dy's type, dweight
+    float32 [cols]). `h` is the normed tensor in dy's type or its Checkpoint;
+    `dresidual` is added to dx; `dweight` False leaves it out (None returned)."""
+    dy = _real2d(dy, "dy")
+    rows, cols = dy.shape
+    dev, dt = dy.device, dy.dtype
+    ckpt = None
+    if isinstance(h, Checkpoint):
+        ckpt, h = _checkpoint_in(h, rows, cols), None
+    else:
+        h = _like(h, dy.shape, dt, "h")
+    weight = _like(weight, (cols,), dt, "weight")
+    rstd = _like(rstd, (rows,), torch.float32, "rstd")
+    dresidual = _like(dresidual, dy.shape, dt, "dresidual")
+    dx = _out(dx, dy.shape, dt, dev, "dx")
+    dweight = None if dweight is False else _out(dweight, (cols,), torch.float32, dev, "dweight")
+    lib = load()
+    if workspace is None and dweight is not None:
+        workspace = _sum_workspace(dev, int(lib.hq_rmsnorm_backward_workspace_bytes(_XT[dt], rows, cols)))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(lib.hq_rmsnorm_backward(dy.data_ptr(), _addr(h), _checkpoint_c(ckpt), _addr(weight), rstd.data_ptr(),
+                                  _addr(dresidual), _XT[dt], rows, cols, dx.data_ptr(), _addr(dweight), _addr(workspace),
+                                  ws_bytes, _stream(dev, stream)))
+    return dx, dweight
+
+
+@_on_stream
+def hq_gemm_a8w8_fused(xq: torch.Tensor, xf: int, wq_pre: torch.Tensor, wf: int, x_scale: torch.Tensor,
+                       w_scale: torch.Tensor, n: int, *, bias: torch.Tensor | None = None,
+                       bias_type: int = HQ_BIAS_BF16, bias_scale: torch.Tensor | None = None, act: int = HQ_ACT_NONE,
+                       residual: torch.Tensor | None = None, out_scale: torch.Tensor | None = None,
+                       out_fmt: int = HQ_E4M3, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """hq_gemm_a8w8_epilogue with act(v + bias) and a bf16 residual [m, n] added
+    after it. `out` (bf16) may be the residual itself. Returns out."""
+    xq, x_scale, w_scale = xq.contiguous(), x_scale.contiguous(), w_scale.contiguous()
+    m, k = xq.shape
+    dev = xq.device
+    if bias is not None:
+        if bias.numel() != n or (bias_type == HQ_BIAS_BF16 and bias.dtype != torch.bfloat16):
+            raise ValueError("bias must have n elements, bf16 unless bias_type says FP8 codes")
+        bias = bias.contiguous()
+    residual = _like(residual, (m, n), torch.bfloat16, "residual")
+    out = _out(out, (m, n), torch.bfloat16 if out_scale is None else torch.uint8, dev, "out")
+    lib = load()
+    if workspace is None:
+        workspace = gemm_workspace(dev, int(lib.hq_gemm_workspace_bytes(m, n, k)))
+    elif workspace is False:
+        workspace = None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ep = hq_fused_epilogue(_addr(bias), int(bias_type), _addr(bias_scale), _addr(out_scale), int(out_fmt), int(act),
+                           _addr(residual))
+    check(lib.hq_gemm_a8w8_fused(xq.data_ptr(), xf, wq_pre.data_ptr(), wf, x_scale.data_ptr(), x_scale.numel(),
+                                 w_scale.data_ptr(), w_scale.numel(), m, n, k, ctypes.byref(ep), out.data_ptr(),
+                                 _addr(workspace), ws_bytes, _stream(dev, stream)))
+    return out
+
+
+@_on_stream
+def hq_act_quantize_fp8(z: torch.Tensor, act: int, fmt: int = HQ_E4M3, *, gated: bool = False, checkpoint=None, q=None,
+                        scale_out=None, stream=None):
+    """act(z), or gated act(z[:, :cols]) * z[:, cols:], quantized per token: returns
+    (q uint8 [rows, cols], scale float32 [rows], Checkpoint of z or None).
+    `checkpoint`: a block size or a Checkpoint whose buffers receive z in 8 bits."""
+    z = _real2d(z, "z")
+    rows, wide = z.shape
+    if gated and wide % 2:
+        raise ValueError("a gated z has an even number of columns")
+    cols = wide // 2 if gated else wide
+    dev = z.device
+    q = _out(q, (rows, cols), torch.uint8, dev, "q")
+    scale_out = _out(scale_out, (rows,), torch.float32, dev, "scale_out")
+    ckpt = _checkpoint_out(checkpoint, rows, wide, dev)
+    check(load().hq_act_quantize_fp8(z.data_ptr(), _XT[z.dtype], rows, cols, act, int(gated), fmt, q.data_ptr(),
+                                     scale_out.data_ptr(), _checkpoint_c(ckpt), _stream(dev, stream)))
+    return q, scale_out, ckpt
+
+
+def hq_act_backward_workspace_bytes(xt: int, rows: int, cols: int, gated: bool) -> int:
+    return int(load().hq_act_backward_workspace_bytes(xt, rows, cols, int(gated)))
+
+
+@_on_stream
+def hq_act_backward(da: torch.Tensor, z: Checkpoint, act: int, *, gated: bool = False, dz=None, dbias=None,
+                    workspace=None, stream=None):
+    """Backward pass of hq_act_quantize_fp8 from z's checkpoint: returns (dz of da's
+    type and z's shape, dbias float32 of z's width); `dbias` False leaves the sum
+    over rows out (None returned)."""
+    da = _real2d(da, "da")
+    rows, cols = da.shape
+    wide = 2 * cols if gated else cols
+    dev, dt = da.device, da.dtype
+    z = _checkpoint_in(z, rows, wide)
+    dz = _out(dz, (rows, wide), dt, dev, "dz")
+    dbias = None if dbias is False else _out(dbias, (wide,), torch.float32, dev, "dbias")
+    lib = load()
+    if workspace is None and dbias is not None:
+        workspace = _sum_workspace(dev, int(lib.hq_act_backward_workspace_bytes(_XT[dt], rows, cols, int(gated))))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(lib.hq_act_backward(da.data_ptr(), _checkpoint_c(z), _XT[dt], rows, cols, act, int(gated), dz.data_ptr(),
+                              _addr(dbias), _addr(workspace), ws_bytes, _stream(dev, stream)))
+    return dz, dbias
+
+
+def hq_wgrad_workspace_bytes(m: int, n: int, k: int, dwt: int) -> int:
+    return int(load().hq_wgrad_workspace_bytes(m, n, k, dwt))
+
+
+@_on_stream
+def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                base: torch.Tensor | None = None, dw=None, workspace=None, stream=None) -> torch.Tensor:
+    """dw[n, k] = base + sum_m g[m, n] x_scale[m] dec(xq[m, k]) from a bf16 gradient
+    g [m, n] and the codes xq [m, k] that the forward GEMM read; dw of `dtype`
+    (bfloat16 or float32; a float32 base only with float32, and dw may be base).
+    `workspace`: None (a shared buffer of the size the shape wants), False (none) or
+    a uint8 tensor."""
+    if g.dim() != 2 or g.dtype != torch.bfloat16:
+        raise ValueError("g must be a 2-D bfloat16 tensor [m, n]")
+    if dtype not in _XT:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    g = g.contiguous()
+    m, n = g.shape
+    if xq.dim() != 2 or xq.shape[0] != m or xq.dtype != torch.uint8:
+        raise ValueError("xq must be uint8 codes [m, k]")
+    if x_scale.dtype != torch.float32:
+        raise ValueError("x_scale must be float32")
+    xq, x_scale = xq.contiguous(), x_scale.contiguous()
+    k = xq.shape[1]
+    dev = g.device
+    base = _like(base, (n, k), torch.float32, "base")
+    dw = _out(dw, (n, k), dtype, dev, "dw")
+    lib = load()
+    if workspace is None:
+        workspace = _sum_workspace(dev, int(lib.hq_wgrad_workspace_bytes(m, n, k, _XT[dtype])))
+    elif workspace is False:
+        workspace = None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(lib.hq_wgrad_a8(g.data_ptr(), xq.data_ptr(), xf, x_scale.data_ptr(), x_scale.numel(), m, n, k, _addr(base),
+                          dw.data_ptr(), _XT[dtype], _addr(workspace), ws_bytes, _stream(dev, stream)))
+    return dw

@@ -21,12 +21,13 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhq.so")
 
-SOURCES = ["quantize.hip", "gemm.hip", "blockscaled.hip", "probe.hip", "hq_api.cpp"]
+SOURCES = ["quantize.hip", "gemm.hip", "gemm_fused.hip", "blockscaled.hip", "norm.hip", "act.hip", "wgrad.hip", "probe.hip",
+           "hq_api.cpp"]
 
 # Per-source flags. The GEMM keeps its MFMA accumulators in VGPRs and the
 # operand fragments in AGPRs: with 256 accumulator registers per wavefront the
 # default AGPR-accumulator allocation spills to scratch, this form does not.
-EXTRA = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "blockscaled.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("gemm.hip", "gemm_fused.hip", "blockscaled.hip")}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -106,6 +106,19 @@ hq_status launched(hipError_t e, const char* what) {
 }
 
 bool valid_fmt(int f) { return f == HQ_E4M3 || f == HQ_E5M2; }
+bool valid_act(int a) { return a >= HQ_ACT_NONE && a <= HQ_ACT_SILU; }
+
+// Fails where one of the first `outs` ranges overlaps any other range.
+hq_status check_outputs(const Range* r, int n, int outs) {
+  for (int i = 0; i < outs; ++i) {
+    const char* other = nullptr;
+    for (int j = i + 1; j < n; ++j) {
+      const Range pair[] = {r[i], r[j]};
+      if (const char* a = find_overlap(pair, 2, &other)) return fail(HQ_ERR_INVALID_ARGUMENT, "%s overlaps %s", a, other);
+    }
+  }
+  return HQ_OK;
+}
 
 int64_t padded_bytes(int64_t n, int64_t k) { return ((n + 31) / 32 * 32) * ((k + 127) / 128 * 128); }
 
@@ -505,7 +518,8 @@ hq_status hq_gemm_a8w8(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf,
 static hq_status gemm_impl(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
                            int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
                            int64_t k, const hq_epilogue* ep, void* out, void* workspace, size_t workspace_bytes,
-                           bool strict, const char* name, hipStream_t stream, bool library_scratch = false) {
+                           bool strict, const char* name, hipStream_t stream, bool library_scratch = false,
+                           const hq_fused_epilogue* fused = nullptr) {
   hq_status st = check_gemm_common(xf, wf, m, n, k);
   if (st != HQ_OK) return st;
   if (workspace_bytes > 0 && workspace == nullptr)
@@ -526,6 +540,8 @@ static hq_status gemm_impl(const uint8_t* xq, int xf, const uint8_t* wq_pre, int
     return fail(HQ_ERR_INVALID_ARGUMENT, "xq, wq_pre, x_scale, w_scale and out must be non-NULL");
   if (!aligned(xq, 16) || !aligned(wq_pre, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "xq and wq_pre must be 16-byte aligned");
   if (!aligned(out, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned");
+  const uint16_t* residual = fused ? fused->residual : nullptr;
+  if (residual && !aligned(residual, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "residual must be 16-byte aligned");
   if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || (bias_scale && !aligned(bias_scale, 4)) ||
       (out_scale && !aligned(out_scale, 4)) || (bias_kind == hq::kBiasBF16 && !aligned(bias, 2)))
     return fail(HQ_ERR_INVALID_ARGUMENT, "scales must be 4-byte aligned and a bf16 bias 2-byte aligned");
@@ -540,9 +556,11 @@ static hq_status gemm_impl(const uint8_t* xq, int xf, const uint8_t* wq_pre, int
       {bias, bias ? (size_t)n * (bias_kind == hq::kBiasBF16 ? 2 : 1) : 0, "bias"},
       {bias_scale, bias_scale ? 4u : 0u, "bias_scale"},
       {out_scale, out_scale ? 4u : 0u, "out_scale"},
+      // a bf16 out may be the residual's own buffer (each value is read before it is written)
+      {residual, residual && (residual != out || out_scale) ? (size_t)m * (size_t)n * 2 : 0, "residual"},
   };
   const char* other = nullptr;
-  const char* a = find_overlap(rg, 9, &other);
+  const char* a = find_overlap(rg, 10, &other);
   if (a && (strcmp(a, "out") == 0 || strcmp(a, "workspace") == 0))
     return fail(HQ_ERR_INVALID_ARGUMENT, "%s overlaps %s", a, other);
   size_t scratch_need = 0;
@@ -559,6 +577,11 @@ static hq_status gemm_impl(const uint8_t* xq, int xf, const uint8_t* wq_pre, int
                  bias, bias_kind, bias_scale, out_scale, out_fmt};
   g.strict = strict;
   (void)hipGetLastError();
+  if (fused) {
+    g.act = fused->act;
+    g.residual = residual;
+    return launched(hq::launch_gemm_fused(g, xf, wf, ws_used ? workspace : nullptr, ws_used, stream), name);
+  }
   if (library_scratch) {
     void* scratch = nullptr;
     if (scratch_need > 0) {
@@ -759,6 +782,285 @@ hq_status hq_gemm_a8w8_blockscaled_preshuffled(const uint8_t* xq, int xf, const 
                  bias, bias ? hq::kBiasBF16 : hq::kBiasNone, nullptr, nullptr, 0, (int)nb};
   (void)hipGetLastError();
   return launched(hq::launch_gemm_bsf(g, xf, wf, block_size, stream), "hq_gemm_a8w8_blockscaled_preshuffled");
+}
+
+hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
+                             int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
+                             int64_t k, const hq_fused_epilogue* ep, void* out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  if (!ep) return fail(HQ_ERR_INVALID_ARGUMENT, "ep must be non-NULL");
+  if (!valid_act(ep->act)) return fail(HQ_ERR_INVALID_ARGUMENT, "unknown activation %d", ep->act);
+  const hq_epilogue base = {ep->bias, ep->bias_type, ep->bias_scale, ep->out_scale, ep->out_fmt};
+  return gemm_impl(xq, xf, wq_pre, wf, x_scale, x_scale_count, w_scale, w_scale_count, m, n, k, &base, out, workspace,
+                   workspace_bytes, false, "hq_gemm_a8w8_fused", stream, false, ep);
+}
+
+// Sizes of the row operators; `wide` is the longest row among the call's tensors.
+static hq_status check_rows(int xt, int64_t rows, int64_t cols, int64_t wide) {
+  if (xt != HQ_F32 && xt != HQ_BF16) return fail(HQ_ERR_INVALID_ARGUMENT, "xt must be HQ_F32 or HQ_BF16, got %d", xt);
+  if (rows < 0 || rows > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^31 - 1024], got %lld", (long long)rows);
+  if (cols < 16 || cols % 16 != 0 || wide > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "cols must be a positive multiple of 16, a row at most 2^31 - 1024 elements, got %lld",
+                (long long)cols);
+  if ((double)rows * (double)wide > 1099511627776.0) return fail(HQ_ERR_INVALID_ARGUMENT, "rows * cols exceeds 2^40");
+  return HQ_OK;
+}
+
+// Block size and, where there are rows, the buffers of a checkpoint of a tensor
+// whose blocks must divide `unit` columns (0: any).
+static hq_status check_checkpoint(const hq_checkpoint* c, int64_t rows, int64_t unit) {
+  if (c->block_size != 32 && c->block_size != 64 && c->block_size != 128)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "the checkpoint's block_size must be 32, 64 or 128, got %d", c->block_size);
+  if (unit && unit % c->block_size != 0)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "gated: cols must be a multiple of the checkpoint's block_size %d, got %lld",
+                c->block_size, (long long)unit);
+  if (rows == 0) return HQ_OK;
+  if (!c->q || !c->scales) return fail(HQ_ERR_INVALID_ARGUMENT, "the checkpoint's q and scales must be non-NULL");
+  if (!aligned(c->q, 16) || !aligned(c->scales, 4))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "the checkpoint's q must be 16-byte and its scales 4-byte aligned");
+  return HQ_OK;
+}
+
+static size_t checkpoint_scale_bytes(const hq_checkpoint* c, int64_t rows, int64_t wide) {
+  return (size_t)rows * (size_t)((wide + c->block_size - 1) / c->block_size) * 4;
+}
+
+hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, int xt, int64_t rows,
+                                  int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out, void* h_out,
+                                  float* rstd_out, const hq_checkpoint* ckpt, hipStream_t stream) {
+  hq_status st = check_rows(xt, rows, cols, cols);
+  if (st != HQ_OK) return st;
+  if (!valid_fmt(fmt)) return fail(HQ_ERR_INVALID_ARGUMENT, "fmt must be HQ_E4M3 or HQ_E5M2, got %d", fmt);
+  if (!(eps >= 0.0f && eps <= 3.4028235e38f)) return fail(HQ_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
+  if (ckpt) {
+    st = check_checkpoint(ckpt, rows, 0);
+    if (st != HQ_OK) return st;
+  }
+  if (rows == 0) return ok();
+  if (!x || !q || !scale_out) return fail(HQ_ERR_INVALID_ARGUMENT, "x, q and scale_out must be non-NULL");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(q, 16) || !aligned(h_out, 16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x, residual, weight, q and h_out must be 16-byte aligned");
+  if (!aligned(scale_out, 4) || !aligned(rstd_out, 4))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "scale_out and rstd_out must be 4-byte aligned");
+  const size_t numel = (size_t)rows * (size_t)cols, es = xt == HQ_BF16 ? 2 : 4;
+  // the outputs first; h_out may be x or the residual itself
+  const Range rg[] = {
+      {q, numel, "q"},
+      {scale_out, (size_t)rows * 4, "scale_out"},
+      {h_out, numel * es, "h_out"},
+      {rstd_out, (size_t)rows * 4, "rstd_out"},
+      {ckpt ? ckpt->q : nullptr, numel, "checkpoint q"},
+      {ckpt ? ckpt->scales : nullptr, ckpt ? checkpoint_scale_bytes(ckpt, rows, cols) : 0, "checkpoint scales"},
+      {x == h_out ? nullptr : x, numel * es, "x"},
+      {residual == h_out ? nullptr : residual, numel * es, "residual"},
+      {weight, (size_t)cols * es, "weight"},
+  };
+  st = check_outputs(rg, 9, 6);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::NormArgs a{x, residual, weight, h_out, q, scale_out, rstd_out, ckpt ? ckpt->q : nullptr,
+                       ckpt ? ckpt->scales : nullptr, (int)rows, (int)cols, ckpt ? ckpt->block_size : 0, fmt, eps};
+  return launched(hq::launch_rmsnorm_quant(a, xt, stream), "hq_rmsnorm_quantize_fp8");
+}
+
+size_t hq_rmsnorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols) {
+  if ((xt != HQ_F32 && xt != HQ_BF16) || rows < 1 || cols < 16 || cols % 16 != 0 || rows > kMaxDim || cols > kMaxDim) return 0;
+  return hq::rmsnorm_bwd_workspace_bytes((int)rows, (int)cols, xt);
+}
+
+// The workspace of a backward pass that sums over rows; `need` 0 without the sum.
+static hq_status check_sum_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
+  if (need == 0) return HQ_OK;
+  if (!workspace || workspace_bytes < need)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "workspace needs %zu bytes, got %zu%s", need, workspace_bytes,
+                workspace ? "" : " (NULL)");
+  if (!aligned(workspace, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  return HQ_OK;
+}
+
+hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
+                              const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
+                              float* dweight, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  hq_status st = check_rows(xt, rows, cols, cols);
+  if (st != HQ_OK) return st;
+  if (ckpt) {
+    st = check_checkpoint(ckpt, rows, 0);
+    if (st != HQ_OK) return st;
+  }
+  if (rows > 0 && (h != nullptr) == (ckpt != nullptr)) return fail(HQ_ERR_INVALID_ARGUMENT, "give h or ckpt, not both");
+  if (!aligned(dweight, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "dweight must be 16-byte aligned");
+  size_t need = 0;
+  if (rows > 0) {
+    if (!dy || !rstd || !dx) return fail(HQ_ERR_INVALID_ARGUMENT, "dy, rstd and dx must be non-NULL");
+    if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dresidual, 16) || !aligned(dx, 16))
+      return fail(HQ_ERR_INVALID_ARGUMENT, "dy, h, weight, dresidual and dx must be 16-byte aligned");
+    if (!aligned(rstd, 4)) return fail(HQ_ERR_INVALID_ARGUMENT, "rstd must be 4-byte aligned");
+    need = dweight ? hq::rmsnorm_bwd_workspace_bytes((int)rows, (int)cols, xt) : 0;
+    st = check_sum_workspace(workspace, workspace_bytes, need);
+    if (st != HQ_OK) return st;
+    const size_t numel = (size_t)rows * (size_t)cols, es = xt == HQ_BF16 ? 2 : 4;
+    const Range rg[] = {
+        {dx, numel * es, "dx"},
+        {dweight, (size_t)cols * 4, "dweight"},
+        {workspace, need, "workspace"},
+        {dy == dx ? nullptr : dy, numel * es, "dy"},
+        {h, numel * es, "h"},
+        {ckpt ? ckpt->q : nullptr, numel, "checkpoint q"},
+        {ckpt ? ckpt->scales : nullptr, ckpt ? checkpoint_scale_bytes(ckpt, rows, cols) : 0, "checkpoint scales"},
+        {weight, (size_t)cols * es, "weight"},
+        {rstd, (size_t)rows * 4, "rstd"},
+        {dresidual == dx ? nullptr : dresidual, numel * es, "dresidual"},
+    };
+    st = check_outputs(rg, 10, 3);
+    if (st != HQ_OK) return st;
+  } else if (!dweight) {
+    return ok();
+  }
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::NormBwdArgs a{dy, h, ckpt ? ckpt->q : nullptr, ckpt ? ckpt->scales : nullptr, weight, rstd, dresidual, dx,
+                          dweight, dweight ? static_cast<float*>(workspace) : nullptr, (int)rows, (int)cols,
+                          ckpt ? ckpt->block_size : 0};
+  return launched(hq::launch_rmsnorm_bwd(a, xt, stream), "hq_rmsnorm_backward");
+}
+
+static hq_status check_act(int act, int gated) {
+  if (!valid_act(act) || act == HQ_ACT_NONE)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "act must be HQ_ACT_RELU, _GELU, _GELU_TANH or _SILU, got %d", act);
+  if (gated != 0 && gated != 1) return fail(HQ_ERR_INVALID_ARGUMENT, "gated must be 0 or 1, got %d", gated);
+  return HQ_OK;
+}
+
+hq_status hq_act_quantize_fp8(const void* z, int xt, int64_t rows, int64_t cols, int act, int gated, int fmt, uint8_t* q,
+                              float* scale_out, const hq_checkpoint* ckpt, hipStream_t stream) {
+  hq_status st = check_act(act, gated);
+  if (st != HQ_OK) return st;
+  const int64_t wide = cols <= kMaxDim && gated ? 2 * cols : cols;
+  st = check_rows(xt, rows, cols, wide);
+  if (st != HQ_OK) return st;
+  if (!valid_fmt(fmt)) return fail(HQ_ERR_INVALID_ARGUMENT, "fmt must be HQ_E4M3 or HQ_E5M2, got %d", fmt);
+  if (ckpt) {
+    st = check_checkpoint(ckpt, rows, gated ? cols : 0);
+    if (st != HQ_OK) return st;
+  }
+  if (rows == 0) return ok();
+  if (!z || !q || !scale_out) return fail(HQ_ERR_INVALID_ARGUMENT, "z, q and scale_out must be non-NULL");
+  if (!aligned(z, 16) || !aligned(q, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "z and q must be 16-byte aligned");
+  if (!aligned(scale_out, 4)) return fail(HQ_ERR_INVALID_ARGUMENT, "scale_out must be 4-byte aligned");
+  const size_t numel = (size_t)rows * (size_t)cols, zn = (size_t)rows * (size_t)wide, es = xt == HQ_BF16 ? 2 : 4;
+  const Range rg[] = {
+      {q, numel, "q"},
+      {scale_out, (size_t)rows * 4, "scale_out"},
+      {ckpt ? ckpt->q : nullptr, zn, "checkpoint q"},
+      {ckpt ? ckpt->scales : nullptr, ckpt ? checkpoint_scale_bytes(ckpt, rows, wide) : 0, "checkpoint scales"},
+      {z, zn * es, "z"},
+  };
+  st = check_outputs(rg, 5, 4);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::ActArgs a{z, q, scale_out, ckpt ? ckpt->q : nullptr, ckpt ? ckpt->scales : nullptr, (int)rows, (int)cols,
+                      ckpt ? ckpt->block_size : 0, fmt};
+  return launched(hq::launch_act_quant(a, xt, act, gated != 0, stream), "hq_act_quantize_fp8");
+}
+
+size_t hq_act_backward_workspace_bytes(int xt, int64_t rows, int64_t cols, int gated) {
+  if ((xt != HQ_F32 && xt != HQ_BF16) || rows < 1 || cols < 16 || cols % 16 != 0 || rows > kMaxDim || cols > kMaxDim) return 0;
+  return hq::act_bwd_workspace_bytes((int)rows, (int)cols, xt, gated != 0);
+}
+
+hq_status hq_act_backward(const void* da, const hq_checkpoint* ckpt, int xt, int64_t rows, int64_t cols, int act,
+                          int gated, void* dz, float* dbias, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  hq_status st = check_act(act, gated);
+  if (st != HQ_OK) return st;
+  const int64_t wide = cols <= kMaxDim && gated ? 2 * cols : cols;
+  st = check_rows(xt, rows, cols, wide);
+  if (st != HQ_OK) return st;
+  if (!ckpt) return fail(HQ_ERR_INVALID_ARGUMENT, "ckpt must be non-NULL");
+  st = check_checkpoint(ckpt, rows, gated ? cols : 0);
+  if (st != HQ_OK) return st;
+  if (!aligned(dbias, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "dbias must be 16-byte aligned");
+  if (rows > 0) {
+    if (!da || !dz) return fail(HQ_ERR_INVALID_ARGUMENT, "da and dz must be non-NULL");
+    if (!aligned(da, 16) || !aligned(dz, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "da and dz must be 16-byte aligned");
+    const size_t need = dbias ? hq::act_bwd_workspace_bytes((int)rows, (int)cols, xt, gated != 0) : 0;
+    st = check_sum_workspace(workspace, workspace_bytes, need);
+    if (st != HQ_OK) return st;
+    const size_t numel = (size_t)rows * (size_t)cols, zn = (size_t)rows * (size_t)wide, es = xt == HQ_BF16 ? 2 : 4;
+    const Range rg[] = {
+        {dz, zn * es, "dz"},
+        {dbias, (size_t)wide * 4, "dbias"},
+        {workspace, need, "workspace"},
+        {da, numel * es, "da"},
+        {ckpt->q, zn, "checkpoint q"},
+        {ckpt->scales, checkpoint_scale_bytes(ckpt, rows, wide), "checkpoint scales"},
+    };
+    st = check_outputs(rg, 6, 3);
+    if (st != HQ_OK) return st;
+  } else if (!dbias) {
+    return ok();
+  }
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::ActBwdArgs a{da, ckpt->q, ckpt->scales, dz, dbias, dbias ? static_cast<float*>(workspace) : nullptr,
+                         (int)rows, (int)cols, ckpt->block_size};
+  return launched(hq::launch_act_bwd(a, xt, act, gated != 0, stream), "hq_act_backward");
+}
+
+static bool wgrad_sizes(int64_t m, int64_t n, int64_t k) {
+  return m >= 0 && n >= 0 && k >= 0 && m <= kMaxDim && n <= kMaxDim && k <= kMaxDim && n % 8 == 0 && k % 16 == 0 &&
+         (double)m * n < 1099511627776.0 && (double)m * k < 1099511627776.0 && (double)n * k < 1099511627776.0;
+}
+
+int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt) {
+  if (!wgrad_sizes(m, n, k) || (dwt != HQ_BF16 && dwt != HQ_F32)) return -1;
+  if (m == 0 || n == 0 || k == 0) return 0;
+  return (int64_t)hq::wgrad_workspace_bytes((int)m, (int)n, (int)k, dwt == HQ_F32);
+}
+
+hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                      int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_fmt(xf)) return fail(HQ_ERR_INVALID_ARGUMENT, "xf must be HQ_E4M3 or HQ_E5M2, got %d", xf);
+  if (dwt != HQ_BF16 && dwt != HQ_F32) return fail(HQ_ERR_INVALID_ARGUMENT, "dwt must be HQ_F32 or HQ_BF16, got %d", dwt);
+  if (!wgrad_sizes(m, n, k))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "m, n, k must be in [0, 2^31 - 1024] with n %% 8 == 0, k %% 16 == 0 and every "
+                "tensor below 2^40 elements, got %lld, %lld, %lld", (long long)m, (long long)n, (long long)k);
+  if (x_scale_count != 1 && x_scale_count != m)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x_scale_count must be 1 or m (%lld), got %lld", (long long)m, (long long)x_scale_count);
+  if (base && dwt != HQ_F32) return fail(HQ_ERR_INVALID_ARGUMENT, "base needs a float32 dw");
+  if (workspace_bytes > 0 && workspace == nullptr)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "workspace is NULL but workspace_bytes is %zu", workspace_bytes);
+  if (workspace_bytes > 0 && !aligned(workspace, 16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  if (n == 0 || k == 0) return ok();
+  if (!dw || (m > 0 && (!g || !xq || !x_scale)))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "g, xq, x_scale and dw must be non-NULL");
+  if (!aligned(g, 16) || !aligned(xq, 16) || !aligned(base, 16) || !aligned(dw, 16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "g, xq, base and dw must be 16-byte aligned");
+  if (!aligned(x_scale, 4)) return fail(HQ_ERR_INVALID_ARGUMENT, "x_scale must be 4-byte aligned");
+  const size_t nk = (size_t)n * (size_t)k;
+  const Range rg[] = {
+      {dw, nk * (dwt == HQ_F32 ? 4 : 2), "dw"},
+      {workspace, workspace_bytes, "workspace"},
+      {g, (size_t)m * (size_t)n * 2, "g"},
+      {xq, (size_t)m * (size_t)k, "xq"},
+      {x_scale, m ? (size_t)x_scale_count * 4 : 0, "x_scale"},
+      {base == dw ? nullptr : base, nk * 4, "base"},
+  };
+  hq_status st = check_outputs(rg, 6, 2);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::WgradArgs a{g, xq, x_scale, base, dw, (int)m, (int)n, (int)k, x_scale_count != 1, dwt == HQ_F32};
+  return launched(hq::launch_wgrad(a, xf, workspace_bytes ? workspace : nullptr, workspace_bytes, stream), "hq_wgrad_a8");
 }
 
 }  // extern "C"

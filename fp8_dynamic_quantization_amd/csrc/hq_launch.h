@@ -101,6 +101,10 @@ struct GemmArgs {
   // matrix-core instructions, which keep every product bit, instead of the FP8
   // ones, whose 8-product runs drop bits 13 below the run's largest exponent.
   int strict;
+  // Fused form only (launch_gemm_fused): activation (kAct*) after the bias, then
+  // the residual's addition; out may be the residual's buffer.
+  int act;
+  const uint16_t* residual;  // bf16 [m, n] or null
 };
 
 // Decode-shape (small M) launch plan: MB 16-row activation blocks, F weight
@@ -120,6 +124,8 @@ SkinnyPlan skinny_plan(int m, int n, int k);
 // are left zero by every launch.
 size_t gemm_workspace_bytes(int m, int n, int k);
 hipError_t launch_gemm(const GemmArgs& a, int xf, int wf, void* workspace, size_t workspace_bytes, hipStream_t st);
+
+hipError_t launch_gemm_fused(const GemmArgs& a, int xf, int wf, void* workspace, size_t workspace_bytes, hipStream_t st);
 
 // Library-held GEMM scratch for callers that cannot allocate: a file-scope
 // device array of kNoAllocScratchBytes per GPU (the largest split plan needs
@@ -154,5 +160,77 @@ hipError_t launch_gemm_bsf(const GemmArgs& a, int xf, int wf, int bs, hipStream_
 // wq_pre + e * preshuffled_bytes(n, k) and scales w_scale + e * (per_col ? n : 1).
 hipError_t launch_grouped_gemm(const GemmArgs& a, const int32_t* offsets, int experts, int xf, int wf,
                                hipStream_t st);
+
+// Sums of `parts` partial rows [parts, cols] in order; parts == 0 gives zeros.
+hipError_t launch_column_sums(const float* partials, int parts, int cols, float* out, hipStream_t st);
+
+// RMS norm with residual and FP8 output. Null pointers leave out what they
+// name; cblock is 0 without a checkpoint, else 32, 64 or 128.
+struct NormArgs {
+  const void* x;         // [rows, cols]
+  const void* residual;  // [rows, cols] or null
+  const void* weight;    // [cols] or null (ones)
+  void* h;               // [rows, cols] or null
+  uint8_t* q;            // [rows, cols]
+  float* scale;          // [rows]
+  float* rstd;           // [rows] or null
+  uint8_t* cq;           // checkpoint codes [rows, cols]
+  float* cs;             // checkpoint scales [rows, ceil(cols / cblock)]
+  int rows, cols, cblock, fmt;
+  float eps;
+};
+hipError_t launch_rmsnorm_quant(const NormArgs& a, int xt, hipStream_t st);
+
+struct NormBwdArgs {
+  const void* dy;      // [rows, cols]
+  const void* h;       // [rows, cols], or null with a checkpoint
+  const uint8_t* cq;   // checkpoint codes, or null
+  const float* cs;
+  const void* weight;  // [cols] or null (ones)
+  const float* rstd;   // [rows]
+  const void* dres;    // [rows, cols] or null
+  void* dx;            // [rows, cols]
+  float* dw;           // [cols] or null
+  float* partials;     // workspace, null exactly when dw is
+  int rows, cols, cblock;
+};
+size_t rmsnorm_bwd_workspace_bytes(int rows, int cols, int xt);
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st);
+
+// Activation into FP8 codes; z is [rows, cols], gated [rows, 2 cols].
+struct ActArgs {
+  const void* z;
+  uint8_t* q;    // [rows, cols]
+  float* scale;  // [rows]
+  uint8_t* cq;   // checkpoint of z, as in NormArgs
+  float* cs;
+  int rows, cols, cblock, fmt;
+};
+hipError_t launch_act_quant(const ActArgs& a, int xt, int act, bool gated, hipStream_t st);
+
+struct ActBwdArgs {
+  const void* da;     // [rows, cols]
+  const uint8_t* cq;  // checkpoint of z
+  const float* cs;
+  void* dz;           // [rows, cols], gated [rows, 2 cols]
+  float* db;          // [cols] or [2 cols], or null
+  float* partials;    // workspace, null exactly when db is
+  int rows, cols, cblock;
+};
+size_t act_bwd_workspace_bytes(int rows, int cols, int xt, bool gated);
+hipError_t launch_act_bwd(const ActBwdArgs& a, int xt, int act, bool gated, hipStream_t st);
+
+// Weight gradient from FP8 codes.
+struct WgradArgs {
+  const uint16_t* g;     // bf16 [m, n]
+  const uint8_t* xq;     // [m, k]
+  const float* x_scale;  // [1] or [m]
+  const float* base;     // float32 [n, k] or null
+  void* dw;              // [n, k], bf16 or float32
+  int m, n, k;
+  int x_scale_per_row, out_f32;
+};
+size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32);
+hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st);
 
 }  // namespace hq

@@ -489,6 +489,184 @@ hq_status hq_grouped_gemm_a8w8_strict(const uint8_t* xq, int xf, const uint8_t* 
                                       int64_t total_rows, int64_t n, int64_t k,
                                       const hq_epilogue* ep, void* out, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the GEMM of a transformer's linear layers. Their tensors are
+ * row-major and contiguous, 16-byte aligned, of one element type `xt` (HQ_F32 or
+ * HQ_BF16); all arithmetic is float32 with one rounding per output element.
+ * -------------------------------------------------------------------------- */
+
+/* Activations. HQ_ACT_GELU is x * Phi(x) (the erf form), HQ_ACT_GELU_TANH its
+ * tanh approximation, HQ_ACT_SILU x / (1 + exp(-x)). */
+typedef enum hq_act {
+  HQ_ACT_NONE = 0,
+  HQ_ACT_RELU = 1,
+  HQ_ACT_GELU = 2,
+  HQ_ACT_GELU_TANH = 3,
+  HQ_ACT_SILU = 4
+} hq_act;
+
+/* An activation kept for the backward pass in 8 bits (host struct): E4M3 codes
+ * and block scales of a [rows, cols] tensor by the rule and in the layout of
+ * hq_quantize_fp8_blockwise, value = dec(q) * scale.
+ *   q           device, uint8 [rows, cols], 16-byte aligned
+ *   scales      device, float32 [rows, ceil(cols / block_size)]
+ *   block_size  32, 64 or 128 */
+typedef struct hq_checkpoint {
+  uint8_t* q;
+  float* scales;
+  int32_t block_size;
+} hq_checkpoint;
+
+/* RMS norm with the residual's addition, into per-token FP8 codes (the GEMM's
+ * left operand):
+ *   h    = x + residual                        (x without a residual)
+ *   rstd = 1 / sqrt(mean_c(h^2) + eps)
+ *   y    = fl32(fl32(h * rstd) * weight)       (no product without a weight)
+ *   q, scale_out = the per-token quantization of y, as hq_quantize_fp8
+ * h is used unrounded; a NaN in a row makes the row's codes 0x7F, an Inf makes
+ * its own code 0x7F and the row's others 0.
+ *   x          device, [rows, cols] of xt
+ *   residual   device, [rows, cols] of xt, or NULL
+ *   weight     device, [cols] of xt, or NULL for ones
+ *   q          device, uint8 [rows, cols]; scale_out device, float32 [rows]
+ *   h_out      device, [rows, cols] of xt: h rounded, or NULL. May be x's or the
+ *              residual's own buffer (the stream updated in place)
+ *   rstd_out   device, float32 [rows], or NULL (the backward pass needs it)
+ *   ckpt       host pointer to an hq_checkpoint whose buffers receive h's 8-bit
+ *              block-wise form, or NULL
+ * Requires cols % 16 == 0, rows, cols <= 2^31 - 1024, rows * cols < 2^40, eps >= 0
+ * and finite; no other overlap of an output with another buffer. rows == 0 returns
+ * HQ_OK without a launch. Rows of up to 32768 bf16 (16384 float32) elements are
+ * read once, longer ones three times. */
+hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, int xt, int64_t rows,
+                                  int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out, void* h_out,
+                                  float* rstd_out, const hq_checkpoint* ckpt, hipStream_t stream);
+
+/* Bytes of device workspace hq_rmsnorm_backward needs for dweight: partial sums
+ * of at most 256 rows, [<= 256, cols] float32. 0 for invalid arguments. */
+size_t hq_rmsnorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols);
+
+/* Backward pass of that norm. With xh = h * rstd and t = dy * weight:
+ *   dx      = rstd * (t - xh * mean_c(t * xh)) + dresidual
+ *   dweight = sum over rows of dy * xh
+ * dx is the gradient of x and, since h = x + residual, of the residual too;
+ * dresidual is the gradient that reaches h past the norm.
+ *   dy         device, [rows, cols] of xt: the gradient of y
+ *   h          device, [rows, cols] of xt, or NULL with ckpt
+ *   ckpt       host pointer to h's 8-bit form, or NULL with h (exactly one)
+ *   weight     device, [cols] of xt, or NULL for ones
+ *   rstd       device, float32 [rows], as the forward pass wrote it
+ *   dresidual  device, [rows, cols] of xt, or NULL
+ *   dx         device, [rows, cols] of xt; may be dy's or dresidual's own buffer
+ *   dweight    device, float32 [cols], 16-byte aligned, or NULL. Summed in an order that the
+ *              sizes fix: the same inputs give the same bits
+ *   workspace  device, at least hq_rmsnorm_backward_workspace_bytes(xt, rows, cols)
+ *              bytes, 16-byte aligned; may be NULL without dweight. Needs no
+ *              initial value; calls that share one must not run concurrently
+ * Sizes as in hq_rmsnorm_quantize_fp8. rows == 0 writes zeros to dweight. */
+hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
+                              const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
+                              float* dweight, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Options of the fused epilogue (host struct): those of hq_epilogue, then
+ *   act       an hq_act value
+ *   residual  device bf16 [m, n], 16-byte aligned, or NULL for none */
+typedef struct hq_fused_epilogue {
+  const void* bias;
+  int32_t bias_type;
+  const float* bias_scale;
+  const float* out_scale;
+  int32_t out_fmt;
+  int32_t act;
+  const uint16_t* residual;
+} hq_fused_epilogue;
+
+/* hq_gemm_a8w8_epilogue with an activation and a residual. Per output element,
+ * in float32:
+ *   v = fl32(fl32(acc * x_scale[m]) * w_scale[n])
+ *   v = fl32(v + b[n])            with a bias
+ *   v = act(v)
+ *   v = fl32(v + residual[m, n])  with a residual
+ *   out[m, n] = bf16_rne(v), or with out_scale the FP8 code as in
+ *               hq_gemm_a8w8_epilogue
+ * `ep` is a host pointer and must not be NULL. A bf16 `out` may be the
+ * residual's own buffer. All other arguments, the workspace rule and the
+ * requirements are those of hq_gemm_a8w8_epilogue. */
+hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
+                             int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
+                             int64_t k, const hq_fused_epilogue* ep, void* out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* Activation into per-token FP8 codes (the next GEMM's left operand), keeping
+ * its input in 8 bits for the backward pass:
+ *   a = act(z)                                 z [rows, cols]
+ *   a = act(z[:, :cols]) * z[:, cols:]         z [rows, 2 * cols], gated
+ *   q, scale_out = the per-token quantization of a, as hq_quantize_fp8
+ *   ckpt = the block-wise E4M3 form of z (over the whole width of z)
+ *   z          device, [rows, cols] or [rows, 2 * cols] of xt
+ *   act        an hq_act value other than HQ_ACT_NONE
+ *   gated      0 or 1
+ *   q          device, uint8 [rows, cols]; scale_out device, float32 [rows]
+ *   ckpt       host pointer to an hq_checkpoint to be written, or NULL
+ * Requires cols % 16 == 0 and, gated with a checkpoint, cols % block_size == 0
+ * (no block spans both halves); rows, 2 * cols <= 2^31 - 1024, rows * cols < 2^40;
+ * no output may overlap another buffer. rows == 0 returns HQ_OK without a launch.
+ * Rows of up to 16384 bf16 (8192 float32) elements of `a` are read once, longer
+ * ones twice. */
+hq_status hq_act_quantize_fp8(const void* z, int xt, int64_t rows, int64_t cols, int act, int gated, int fmt, uint8_t* q,
+                              float* scale_out, const hq_checkpoint* ckpt, hipStream_t stream);
+
+/* Bytes of device workspace hq_act_backward needs for dbias. 0 for invalid
+ * arguments. */
+size_t hq_act_backward_workspace_bytes(int xt, int64_t rows, int64_t cols, int gated);
+
+/* Backward pass of that activation from the 8-bit checkpoint, z^ = dec(q) * scale:
+ *   dz = da * act'(z^)                                        z^ [rows, cols]
+ *   dz = [da * z2^ * act'(z1^) | da * act(z1^)]               gated, [rows, 2 * cols]
+ *   dbias = sum over rows of dz, unrounded (the gradient of a bias added to z)
+ *   da         device, [rows, cols] of xt
+ *   ckpt       host pointer to z's 8-bit form
+ *   dz         device, [rows, cols] or [rows, 2 * cols] of xt
+ *   dbias      device, float32 of z's width, 16-byte aligned, or NULL. Summed in an order that
+ *              the sizes fix
+ *   workspace  device, at least hq_act_backward_workspace_bytes(...) bytes,
+ *              16-byte aligned; may be NULL without dbias. Needs no initial value;
+ *              calls that share one must not run concurrently
+ * Sizes as in hq_act_quantize_fp8 (gated: cols % block_size == 0). rows == 0 writes
+ * zeros to dbias. */
+hq_status hq_act_backward(const void* da, const hq_checkpoint* ckpt, int xt, int64_t rows, int64_t cols, int act,
+                          int gated, void* dz, float* dbias, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace worth passing to hq_wgrad_a8 (0: none). Returns -1 for
+ * invalid sizes. */
+int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
+
+/* Weight gradient of a linear layer from the FP8 activation codes that its
+ * forward GEMM read (kept instead of the high-precision activation):
+ *   dw[n, k] = base[n, k] + sum_m g[m, n] * x_scale[m] * dec(XQ[m, k])
+ *   g          device, bf16 bits [m, n]: the gradient of the layer's output
+ *   xq         device, uint8 [m, k] codes in format xf, row-major
+ *   x_scale    device, float32 [x_scale_count], x_scale_count = 1 or m
+ *   base       device, float32 [n, k], or NULL: a gradient to add to (dwt HQ_F32
+ *              only); may be dw's own buffer
+ *   dw         device, [n, k] of dwt (HQ_BF16 or HQ_F32)
+ *   workspace  device, workspace_bytes bytes, 16-byte aligned, or NULL with 0.
+ *              Needs no initial value. With hq_wgrad_workspace_bytes(m, n, k, dwt)
+ *              bytes a gradient of few tiles is split over the tokens; with less it
+ *              is not, slower, and its sums are associated otherwise. Calls that
+ *              share one must not run concurrently
+ * Products run on the bf16 matrix cores with float32 sums. g * x_scale[m] is
+ * rounded to bf16 for a bf16 result (one rounding of 2^-9 per term beside the
+ * result's own); for a float32 result it is carried as two bf16 numbers, exact to
+ * 2^-17 per term, at twice the matrix-core work.
+ * Requires n % 8 == 0, k % 16 == 0, m, n, k <= 2^31 - 1024, m * n, m * k and n * k <
+ * 2^40; 16-byte aligned g, xq, base, dw; no output may overlap an input
+ * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
+ * base, or zeros. */
+hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                      int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
 /* Row-streaming probe: a measurement aid, not a step of the quantization (no
  * page defines it). It moves the bytes of a per-token quantize pass without
  * its arithmetic: for each of `rows` rows of 16-bit elements it writes the
