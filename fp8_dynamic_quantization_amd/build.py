@@ -27,7 +27,7 @@ SOURCES = ["quantize.hip", "gemm.hip", "gemm_fused.hip", "blockscaled.hip", "nor
 # Per-source flags. The GEMM keeps its MFMA accumulators in VGPRs and the
 # operand fragments in AGPRs: with 256 accumulator registers per wavefront the
 # default AGPR-accumulator allocation spills to scratch, this form does not.
-EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("gemm.hip", "gemm_fused.hip", "blockscaled.hip")}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("gemm.hip", "gemm_fused.hip", "blockscaled.hip", "wgrad.hip")}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1114,7 +1114,7 @@ static hipError_t launch_skinny(const GemmArgs& a, void* workspace, size_t works
 // the device.
 enum TileCfg { kTile256, kTile128x256, kTile128, kTile64x128 };
 
-static TileCfg pick_tile(long rows, long n, int experts, bool strict) {
+inline TileCfg pick_tile(long rows, long n, int experts, bool strict) {
   struct Cand {
     TileCfg cfg;
     int bm, bn;

@@ -3,62 +3,334 @@
 //   dW[n, k] = base[n, k] + sum_m G[m, n] * x_scale[m] * dec(XQ[m, k])
 //
 // G bf16 [m, n], XQ uint8 [m, k], both row-major, so the contraction runs over
-// the slow axis of both.
-#include "hq_launch.h"
+// the slow axis of both operands while the matrix cores want 8 consecutive
+// contraction values per lane. Tiles are staged in LDS as they lie in memory
+// (rows of tokens) and transposed on the way out by the LDS transpose reads:
+//   ds_read_tr16_b64  16 lanes read 4 rows x 16 bf16 (lane 4r + c supplies columns
+//                     4c..4c+3 of row r); lane i receives column i of the 4 rows
+//   ds_read_tr8_b64   16 lanes read 8 rows x 16 bytes (lane 2r + c supplies bytes
+//                     8c..8c+7 of row r); lane i receives column i of the 8 rows
+// so one 8-bit and two 16-bit reads give the operands of V_MFMA_F32_16X16X32_BF16,
+// whose lane l holds contraction values 8 (l / 16) .. +7 of row or column l % 16.
+//
+// The FP8 codes are exact in bf16 and are converted after the read. The token's
+// scale is folded into G on its way to LDS, once per workgroup: rounded to bf16
+// (2^-8 of a term at most), or as the sum of two bf16 numbers (hi = bf16(v), lo =
+// bf16(v - hi): 2^-17 of a term is left over) whose products are both added, for
+// a float32 result and wherever few tokens leave little to average the terms'
+// roundings over.
+#include "gemm_kernels.h"
 #include "hq_row.h"
 
 namespace hq {
 
-// A 64 x 64 tile per workgroup, 4 x 4 outputs per thread, 16 tokens staged in
-// LDS at a time as float32.
-template <int XF>
-__global__ __launch_bounds__(256) void wgrad_kernel(WgradArgs a) {
-  __shared__ float sg[16][64], sx[16][64];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t n0 = (int64_t)blockIdx.y * 64, k0 = (int64_t)blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int64_t m0 = 0; m0 < a.m; m0 += 16) {
-    for (int i = tid; i < 1024; i += 256) {
-      const int r = i >> 6, c = i & 63;
-      const int64_t m = m0 + r;
-      float g = 0.0f, x = 0.0f;
-      if (m < a.m) {
-        if (n0 + c < a.n) g = __uint_as_float((uint32_t)a.g[(size_t)m * a.n + n0 + c] << 16) * a.x_scale[a.x_scale_per_row ? m : 0];
-        if (k0 + c < a.k) {
-          const int code = a.xq[(size_t)m * a.k + k0 + c];
-          x = XF == kE4M3 ? __builtin_amdgcn_cvt_f32_fp8(code, 0) : __builtin_amdgcn_cvt_f32_bf8(code, 0);
-        }
-      }
-      sg[r][c] = g;
-      sx[r][c] = x;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sg[r][ty * 4 + i], sx[r][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + ty * 4 + i, k = k0 + tx * 4 + j;
-      if (n >= a.n || k >= a.k) continue;
-      const size_t at = (size_t)n * a.k + k;
-      const float v = a.base ? acc[i][j] + a.base[at] : acc[i][j];
-      if (a.out_f32) static_cast<float*>(a.dw)[at] = v;
-      else static_cast<uint16_t*>(a.dw)[at] = (uint16_t)f32_to_bf16_rne(v);
-    }
+typedef short wg_s4 __attribute__((ext_vector_type(4)));
+typedef int wg_i2 __attribute__((ext_vector_type(2)));
+typedef __bf16 wg_b8 __attribute__((ext_vector_type(8)));
+#define HQ_LDS __attribute__((address_space(3)))
+
+// BN x BK outputs per workgroup of 8 wavefronts. KS = 1: 4 wavefronts along n, 2
+// along k. KS = 2: two groups of 2 x 2 wavefronts, each with its own stages, take
+// the even and the odd steps of MS tokens and meet at the end.
+template <int BN, int BK, int KS, int MS, bool HILO>
+struct WgCfg {
+  static constexpr int kThreads = 512;
+  static constexpr int T = kThreads / KS;           // threads of a group
+  static constexpr int kNW = KS == 1 ? 4 : 2;       // wavefronts along n
+  static constexpr int kKW = 2;                     // along k
+  static constexpr int WN = BN / kNW, WK = BK / kKW;
+  static constexpr int FN = WN / 16, FK = WK / 16;  // fragments per wavefront
+  static constexpr int kGRow = BN * 2, kXRow = BK;  // LDS row bytes
+  static constexpr int kGBytes = MS * kGRow, kXBytes = MS * kXRow;
+  static constexpr int kStage = kGBytes * (HILO ? 2 : 1) + kXBytes;
+  static constexpr int kGVec = MS * (BN / 8) / T, kXVec = MS * (BK / 16) / T;  // 16-byte pieces per thread
+  static constexpr int kGStep = T / (BN / 8), kXStep = T / (BK / 16);          // rows between them
+  static constexpr int kLds = 2 * KS * kStage;
+  static_assert(WN == 64 && (FK == 8 || FK == 4), "the swizzles below assume these");
+  static_assert(kGStep % 8 == 0 && kXStep % 16 == 0, "a thread's pieces share one swizzle");
+  static_assert(KS == 1 || BN * BK * 4 <= kLds, "the second group's sums fit the stages");
+};
+
+// Rows of an LDS tile start on the same bank, so the pieces of a row are permuted
+// by its number: units of 32 bytes of a G row (what a transpose read takes of one
+// row) by row % 8, units of 16 bytes of an X row so that 16 rows cover all banks.
+template <int BK>
+__device__ __forceinline__ int x_swizzle(int row) {
+  return BK == 256 ? row & 15 : (row >> 1) & 7;
 }
 
-size_t wgrad_workspace_bytes(int, int, int, bool) { return 0; }
+template <int XF>
+__device__ __forceinline__ wg_b8 bf16x8(wg_i2 c) {
+  bf2v v[4];
+  if constexpr (XF == kE4M3) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, true);
+  } else {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[0], 1.0f, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[0], 1.0f, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[1], 1.0f, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[1], 1.0f, true);
+  }
+  return wg_b8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
 
-hipError_t launch_wgrad(const WgradArgs& a, int xf, void*, size_t, hipStream_t st) {
-  const dim3 grid((a.k + 63) / 64, (a.n + 63) / 64);
-  if (xf == kE4M3) hipLaunchKernelGGL(wgrad_kernel<kE4M3>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(wgrad_kernel<kE5M2>, grid, dim3(256), 0, st, a);
+// Steps [step0, step1) of MS tokens; `part` selects the partial-sum slab when the
+// tokens are split over workgroups.
+template <int XF, int BN, int BK, int KS, int MS, bool HILO>
+__global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, int tiles_k, int steps_per_part,
+                                                    float* partials) {
+  using C = WgCfg<BN, BK, KS, MS, HILO>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
+  int tn, tk;
+  tile_coords(xcd_remap(blockIdx.x, tiles_n * tiles_k), tiles_n, tiles_k, &tn, &tk);
+  const int n0 = tn * BN, k0 = tk * BK;
+  const int ks = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / C::T);
+  const int t = threadIdx.x - ks * C::T;
+  const int lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wn = wave / C::kKW, wk = wave % C::kKW;
+  const int nsteps_all = (int)(((int64_t)a.m + MS - 1) / MS);
+  const int s_begin = blockIdx.y * steps_per_part;
+  const int s_end = min(nsteps_all, s_begin + steps_per_part);
+
+  // staging: piece v of a thread is row v * step + row0, one 16-byte chunk
+  const int g_c = t % (BN / 8), g_r = t / (BN / 8);
+  const int x_c = t % (BK / 16), x_r = t / (BK / 16);
+  const int g_vo = n0 + g_c * 8 < a.n ? (int)((uint32_t)g_r * (uint32_t)a.n * 2u + (uint32_t)g_c * 16u) : kBadOffset;
+  const int x_vo = k0 + x_c * 16 < a.k ? (int)((uint32_t)x_r * (uint32_t)a.k + (uint32_t)x_c * 16u) : kBadOffset;
+  const int g_dst = g_r * C::kGRow + (((g_c >> 1) ^ (g_r & 7)) << 5) + ((g_c & 1) << 4);
+  const int x_dst = x_r * C::kXRow + ((x_c ^ x_swizzle<BK>(x_r)) << 4);
+  const __amdgpu_buffer_rsrc_t s_rsrc = row_rsrc(a.x_scale, a.x_scale_per_row ? (uint32_t)a.m * 4u : 4u);
+
+  uint4 rg[C::kGVec], rx[C::kXVec];
+  float rs[C::kGVec];
+  // Tokens past m read zeros (past the extents), and so do columns past n and k.
+  auto load = [&](int s) {
+    const int64_t m0 = (int64_t)s * MS;
+    const uint32_t rows = s < s_end ? (uint32_t)min((int64_t)MS, a.m - m0) : 0u;
+    const __amdgpu_buffer_rsrc_t g_rsrc =
+        row_rsrc(a.g + (size_t)(rows ? m0 : 0) * a.n + n0, rows ? rows * (uint32_t)a.n * 2u - (uint32_t)n0 * 2u : 0u);
+    const __amdgpu_buffer_rsrc_t x_rsrc =
+        row_rsrc(a.xq + (size_t)(rows ? m0 : 0) * a.k + k0, rows ? rows * (uint32_t)a.k - (uint32_t)k0 : 0u);
+#pragma unroll
+    for (int v = 0; v < C::kGVec; ++v)
+      rg[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(g_rsrc, g_vo, (int)((uint32_t)(v * C::kGStep) * (uint32_t)a.n * 2u), 0));
+#pragma unroll
+    for (int v = 0; v < C::kXVec; ++v)
+      rx[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_vo, (int)((uint32_t)(v * C::kXStep) * (uint32_t)a.k), 0));
+#pragma unroll
+    for (int v = 0; v < C::kGVec; ++v)
+      rs[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          s_rsrc, !rows ? kBadOffset : a.x_scale_per_row ? ((int)m0 + v * C::kGStep + g_r) * 4 : 0, 0, 0));
+  };
+  uint8_t* const lds_g = lds + ks * 2 * C::kStage;
+  auto store = [&](int buf) {
+    uint8_t* g = lds_g + buf * C::kStage;
+    uint8_t* x = g + C::kGBytes * (HILO ? 2 : 1);
+#pragma unroll
+    for (int v = 0; v < C::kGVec; ++v) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
+        hi[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2v));
+        if constexpr (HILO) {
+          // an infinite or NaN hi carries the value alone
+          const float h0 = bf16_lo(hi[e]), h1 = bf16_hi(hi[e]);
+          const f2v q = {fabsf(h0) < __builtin_inff() ? p[0] - h0 : 0.0f, fabsf(h1) < __builtin_inff() ? p[1] - h1 : 0.0f};
+          lo[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2v));
+        }
+      }
+      *reinterpret_cast<uint4*>(g + g_dst + v * C::kGStep * C::kGRow) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (HILO)
+        *reinterpret_cast<uint4*>(g + C::kGBytes + g_dst + v * C::kGStep * C::kGRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+#pragma unroll
+    for (int v = 0; v < C::kXVec; ++v) *reinterpret_cast<uint4*>(x + x_dst + v * C::kXStep * C::kXRow) = rx[v];
+  };
+
+  // Operand reads. The swizzle only touches address bits below the row, and a
+  // fragment's number only bits of the unit, so a fragment's address is the
+  // lane's base with those bits flipped; rows and sub-steps are constant offsets.
+  const int l16 = lane & 15, grp = lane >> 4;
+  const int g_row = 8 * grp + (l16 >> 2);
+  const int g_rd = g_row * C::kGRow + (((wn * C::FN) ^ (l16 >> 2)) << 5) + ((l16 & 3) << 3);
+  const int x_row = 8 * grp + (l16 >> 1);
+  const int x_rd = x_row * C::kXRow + (((wk * C::FK) ^ x_swizzle<BK>(x_row)) << 4) + ((l16 & 1) << 3);
+
+  v4f acc[C::FK][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FK; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int buf) {
+    const uint8_t* g = lds_g + buf * C::kStage;
+    const uint8_t* x = g + C::kGBytes * (HILO ? 2 : 1);
+#pragma unroll
+    for (int ss = 0; ss < MS / 32; ++ss) {
+      wg_b8 fg[HILO ? 2 : 1][C::FN];
+#pragma unroll
+      for (int h = 0; h < (HILO ? 2 : 1); ++h)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+          const wg_s4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (HQ_LDS wg_s4*)(g + h * C::kGBytes + (g_rd ^ (j << 5)) + ss * 32 * C::kGRow));
+          const wg_s4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (HQ_LDS wg_s4*)(g + h * C::kGBytes + (g_rd ^ (j << 5) ^ (4 << 5)) + (ss * 32 + 4) * C::kGRow));
+          fg[h][j] = __builtin_bit_cast(wg_b8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+#pragma unroll
+      for (int i = 0; i < C::FK; ++i) {
+        const wg_i2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((HQ_LDS wg_i2*)(x + (x_rd ^ (i << 4)) + ss * 32 * C::kXRow));
+        const wg_b8 fx = bf16x8<XF>(c);
+#pragma unroll
+        for (int h = 0; h < (HILO ? 2 : 1); ++h)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fg[h][j], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+
+  // Step s is loaded two steps ahead into registers and stored one step ahead;
+  // both groups of KS == 2 pass the same number of barriers (steps past the end
+  // hold zeros).
+  const int iters = (max(s_end - s_begin, 0) + KS - 1) / KS;
+  load(s_begin + ks);
+  store(0);
+  load(s_begin + ks + KS);
+  __syncthreads();
+  for (int i = 0; i < iters; ++i) {
+    store((i + 1) & 1);
+    load(s_begin + ks + (i + 2) * KS);
+    compute(i & 1);
+    __syncthreads();
+  }
+
+  if constexpr (KS == 2) {
+    v4f* part = reinterpret_cast<v4f*>(lds);
+    if (ks == 1) {
+#pragma unroll
+      for (int i = 0; i < C::FK; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) part[(i * C::FN + j) * C::T + t] = acc[i][j];
+    }
+    __syncthreads();
+    if (ks == 1) return;
+#pragma unroll
+    for (int i = 0; i < C::FK; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] += part[(i * C::FN + j) * C::T + t];
+  }
+
+  // Lane l of fragment (i, j) holds columns k = 16 i + 4 (l / 16) .. +3 of row
+  // n = 16 j + l % 16 of its wavefront's block.
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) {
+    const int n = n0 + wn * C::WN + j * 16 + l16;
+    if (n >= a.n) continue;
+#pragma unroll
+    for (int i = 0; i < C::FK; ++i) {
+      const int k = k0 + wk * C::WK + i * 16 + 4 * grp;
+      if (k >= a.k) continue;
+      const size_t at = (size_t)n * a.k + k;
+      v4f v = acc[i][j];
+      if (partials) {
+        *reinterpret_cast<v4f*>(partials + (size_t)blockIdx.y * a.n * a.k + at) = v;
+        continue;
+      }
+      if (a.base) v += *reinterpret_cast<const v4f*>(a.base + at);
+      if (HILO && a.out_f32) {
+        *reinterpret_cast<v4f*>(static_cast<float*>(a.dw) + at) = v;
+      } else {
+        const bf2v b0 = __builtin_convertvector((f2v{v[0], v[1]}), bf2v), b1 = __builtin_convertvector((f2v{v[2], v[3]}), bf2v);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) =
+            make_uint2(__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1));
+      }
+    }
+  }
+}
+
+// The split form's sums, added in the order of the tokens.
+__global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict__ partials, int parts, size_t nvec,
+                                                        const float* base, void* dw, int out_f32) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= nvec) return;
+  v4f v = reinterpret_cast<const v4f*>(partials)[i];
+  for (int p = 1; p < parts; ++p) v += reinterpret_cast<const v4f*>(partials)[(size_t)p * nvec + i];
+  if (base) v += reinterpret_cast<const v4f*>(base)[i];
+  if (out_f32) {
+    static_cast<v4f*>(dw)[i] = v;
+  } else {
+    const bf2v b0 = __builtin_convertvector((f2v{v[0], v[1]}), bf2v), b1 = __builtin_convertvector((f2v{v[2], v[3]}), bf2v);
+    static_cast<uint2*>(dw)[i] = make_uint2(__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1));
+  }
+}
+
+// Up to this many tokens a bf16 result, too, carries g * scale in two numbers: the
+// call's time is that of writing dW.
+constexpr int kWgTwoNumbersM = 64;
+
+// Launch plan: the 256 x 256 tile where its tiles fill the CUs, else 128 x 128;
+// where those leave CUs idle too and there are many tokens, the tokens are split.
+struct WgPlan {
+  bool big;
+  int tiles_n, tiles_k, steps, parts;
+};
+static WgPlan wgrad_plan(int m, int n, int k, bool hilo) {
+  const int ms = hilo ? 32 : 64;
+  WgPlan p;
+  auto tiles = [&](int b) { return (int64_t)((n + b - 1) / b) * ((k + b - 1) / b); };
+  p.big = tiles(256) >= kNumCUs * 3 / 4;
+  const int b = p.big ? 256 : 128;
+  p.tiles_n = (n + b - 1) / b;
+  p.tiles_k = (k + b - 1) / b;
+  const int nsteps = (int)(((int64_t)m + ms - 1) / ms);
+  p.parts = 1;
+  while (!p.big && tiles(b) * p.parts * 2 <= kNumCUs && nsteps >= p.parts * 2 * 8) p.parts *= 2;
+  p.steps = (nsteps + p.parts - 1) / p.parts;
+  return p;
+}
+
+static bool wgrad_hilo(int m, bool out_f32) { return out_f32 || m <= kWgTwoNumbersM; }
+
+size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32) {
+  const WgPlan p = wgrad_plan(m, n, k, wgrad_hilo(m, out_f32));
+  return p.parts == 1 ? 0 : (size_t)p.parts * n * k * 4;
+}
+
+template <int XF, bool HILO>
+static hipError_t launch_wgrad_t(const WgradArgs& a, void* workspace, size_t workspace_bytes, hipStream_t st) {
+  constexpr int MS = HILO ? 32 : 64;
+  WgPlan p = wgrad_plan(a.m, a.n, a.k, HILO);
+  if (p.parts > 1 && workspace_bytes < (size_t)p.parts * a.n * a.k * 4) {
+    p.steps *= p.parts;
+    p.parts = 1;
+  }
+  float* partials = p.parts > 1 ? static_cast<float*>(workspace) : nullptr;
+  const dim3 grid(p.tiles_n * p.tiles_k, p.parts);
+  if (p.big)
+    hipLaunchKernelGGL((wgrad_kernel<XF, 256, 256, 1, MS, HILO>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
+                       partials);
+  else
+    hipLaunchKernelGGL((wgrad_kernel<XF, 128, 128, 2, MS, HILO>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
+                       partials);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !partials) return e;
+  const size_t nvec = (size_t)a.n * a.k / 4;
+  hipLaunchKernelGGL(wgrad_sum_kernel, dim3((unsigned)((nvec + 255) / 256)), dim3(256), 0, st, partials, p.parts, nvec, a.base,
+                     a.dw, a.out_f32);
   return hipGetLastError();
+}
+
+hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st) {
+  const bool hilo = wgrad_hilo(a.m, a.out_f32);
+  if (xf == kE4M3) return hilo ? launch_wgrad_t<kE4M3, true>(a, workspace, workspace_bytes, st)
+                               : launch_wgrad_t<kE4M3, false>(a, workspace, workspace_bytes, st);
+  return hilo ? launch_wgrad_t<kE5M2, true>(a, workspace, workspace_bytes, st)
+              : launch_wgrad_t<kE5M2, false>(a, workspace, workspace_bytes, st);
 }
 
 }  // namespace hq

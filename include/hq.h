@@ -655,12 +655,11 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
  *              bytes a gradient of few tiles is split over the tokens; with less it
  *              is not, slower, and its sums are associated otherwise. Calls that
  *              share one must not run concurrently
- * Products run on the bf16 matrix cores with float32 sums. g * x_scale[m] is
- * rounded to bf16 for a bf16 result (one rounding of 2^-9 per term beside the
- * result's own); for a float32 result it is carried as two bf16 numbers, exact to
- * 2^-17 per term, at twice the matrix-core work.
- * Requires n % 8 == 0, k % 16 == 0, m, n, k <= 2^31 - 1024, m * n, m * k and n * k <
- * 2^40; 16-byte aligned g, xq, base, dw; no output may overlap an input
+ * Products run on the bf16 matrix cores with float32 sums. For a bf16 result of
+ * more than 64 tokens g * x_scale[m] is rounded to bf16 (at most 2^-8 of a term,
+ * beside the result's own rounding); otherwise it is carried as two bf16 numbers,
+ * exact to 2^-17 of a term, at twice the matrix-core work.
+ * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n, m * k and n * k < 2^40; 16-byte aligned g, xq, base, dw; no output may overlap an input
  * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
  * base, or zeros. */
 hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,

@@ -125,7 +125,7 @@ def test_wgrad_refusals(hq, E):  # noqa: F811
     for bad in (dict(xf=2), dict(dwt=2), dict(m=-1), dict(n=12), dict(k=24), dict(xsc=2), dict(base=fake(3)), dict(g=None),
                 dict(xq=None), dict(xs=None), dict(dw=None), dict(g=fake(0, 8)), dict(xq=fake(1, 4)), dict(dw=fake(4, 4)),
                 dict(dw=fake(0)), dict(dw=fake(1)), dict(base=fake(4, 16), dwt=0), dict(base=fake(3, 4), dwt=0), dict(wsb=64),
-                dict(ws=fake(5, 4), wsb=64), dict(ws=fake(0), wsb=64), dict(xs=fake(2, 2)), dict(m=1 << 31)):
+                dict(ws=fake(5, 4), wsb=64), dict(ws=fake(0), wsb=64), dict(xs=fake(2, 2)), dict(m=1 << 28), dict(n=1 << 24), dict(k=1 << 24)):
         assert _wgrad(hq, **bad) == E, bad
     assert _wgrad(hq, n=0) == hq.HQ_OK and _wgrad(hq, k=0) == hq.HQ_OK
     assert hq.hq_wgrad_workspace_bytes(64, 12, 16, 0) == -1 and hq.hq_wgrad_workspace_bytes(64, 16, 16, 7) == -1
