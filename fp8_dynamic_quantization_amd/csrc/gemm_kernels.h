@@ -37,6 +37,8 @@
 #include "hq_device.h"
 #include "hq_launch.h"
 
+#include <type_traits>
+
 namespace hq {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -167,23 +169,21 @@ __device__ __forceinline__ void fused_values(const GemmArgs& a, float* v, const 
   }
 }
 
-// The residual's N (4 or 8) columns from col0 on of one row; zeros past the
-// tile's rows and the last column (their outputs are not stored).
-template <int N>
-__device__ __forceinline__ uint4 residual_cols(const GemmArgs& a, int row, int row_end, int col0) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (row < row_end && col0 < a.n) {
+// The residual's 4 columns from col0 on of one row (weight-streaming kernel);
+// zeros past the last row and column (their outputs are not stored).
+__device__ __forceinline__ uint4 residual4(const GemmArgs& a, int row, int col0) {
+  uint32_t w[2] = {0u, 0u};
+  if (row < a.m && col0 < a.n) {
     const uint16_t* p = a.residual + (size_t)row * a.n + col0;
-    if (a.n % N == 0) {  // whole vectors, aligned
-      if constexpr (N == 8) return *reinterpret_cast<const uint4*>(p);
+    if (a.n % 4 == 0) {  // whole vectors, aligned
       const uint2 t = *reinterpret_cast<const uint2*>(p);
       return make_uint4(t.x, t.y, 0u, 0u);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < 4; ++e)
       if (col0 + e < a.n) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], 0u, 0u);
 }
 
 // ---------------------------------------------------------------------------
@@ -207,6 +207,130 @@ struct BsCfg {
   static_assert(BM % 32 == 0 && TN % 32 == 0 && kWR % 16 == 0, "tile");
 };
 
+// The fused epilogue of a tile whose K loop has ended on a barrier. The
+// accumulators go through LDS (the A stages) in passes of kPassRows rows as
+// float32, and come back as 8 consecutive columns of a row per thread: the code
+// that applies scales, bias, activation and residual exists once instead of once
+// per fragment (unrolled over 16 fragments it either spilled or no longer
+// unrolled, and 4096^3 took 508 us), a thread's columns are the same in every
+// pass, and the residual is read and the output written in whole lines. LDS costs
+// a pass about 1000 cycles. 16-byte pieces sit at piece ^ (row % 16), so the
+// fragment-order writes and the row-order reads are free of bank conflicts. The
+// residual of the next pass is loaded while this one is computed. Each value's
+// residual is read by the thread that stores it: `out` may be the same buffer.
+template <class C, int WM, int KS>
+__device__ __forceinline__ void fused_epilogue(const GemmArgs& a, uint8_t* lds, v4f (&acc)[C::kIM][C::kIN], int m0,
+                                               int row_end, int n0, int tid, const float* s_xs, const float* s_ws,
+                                               const float* s_bias) {
+  constexpr int kPassRows = 2 * C::kABytes / (C::kBN * 4);
+  constexpr int kWaveRows = kPassRows / WM;   // of each wavefront row
+  constexpr int kFrags = kWaveRows / 16;      // fragments of a wavefront per pass
+  constexpr int kPasses = C::kIM / kFrags;
+  constexpr int kCV = C::kBN / 8;             // 8-column groups per row
+  constexpr int kThreads = KS * C::kThreads;
+  constexpr int kNC = kPassRows * kCV / kThreads;
+  static_assert(kFrags >= 1 && kPasses * kFrags == C::kIM && kNC >= 1 && kThreads % kCV == 0, "passes");
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) & 3);
+  const int wrow = __builtin_amdgcn_readfirstlane((tid % C::kThreads) >> 8);
+  const bool holds = KS == 1 || tid < C::kThreads;  // split K: the first group holds the sums
+  const int c = tid % kCV, r0 = tid / kCV;
+  const int col = n0 + 8 * c;
+  const int left = a.n - col;
+  const bool vec = (a.n & 7) == 0;
+  // Row of the tile that pass row r of pass q holds.
+  auto tile_row = [&](int q, int r) { return (r / kWaveRows) * C::kWR + q * kWaveRows + r % kWaveRows; };
+
+  float wsc[8], bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    wsc[e] = s_ws[8 * c + e];
+    bias[e] = a.bias_kind != kBiasNone ? s_bias[8 * c + e] : 0.0f;
+  }
+  const float r_out = a.out_scale ? 1.0f / a.out_scale[0] : 0.0f;
+  uint4 res[kNC];
+  auto load_res = [&](int q) {
+#pragma unroll
+    for (int p = 0; p < kNC; ++p) {
+      const int row = m0 + tile_row(q, r0 + p * (kThreads / kCV));
+      res[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < row_end && left > 0) {
+        const uint16_t* src = a.residual + (size_t)row * a.n + col;
+        if (vec) {
+          res[p] = *reinterpret_cast<const uint4*>(src);
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < left) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+          res[p] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  };
+  if (a.residual) load_res(0);
+#pragma unroll 1
+  for (int q = 0; q < kPasses; ++q) {
+    if (holds) {
+#pragma unroll
+      for (int qq = 0; qq < kPasses; ++qq) {
+        if (q != qq) continue;  // the accumulators' indices are compile-time
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f) {
+          const int r = wrow * kWaveRows + f * 16 + (lane & 15);
+#pragma unroll
+          for (int j = 0; j < C::kIN; ++j) {
+            const int piece = wave * (C::kIN * 4) + 8 * (j >> 1) + 2 * (lane >> 4) + (j & 1);
+            *reinterpret_cast<v4f*>(lds + r * (C::kBN * 4) + ((piece ^ (r & 15)) << 4)) = acc[qq * kFrags + f][j];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    uint4 cur[kNC];
+#pragma unroll
+    for (int p = 0; p < kNC; ++p) cur[p] = res[p];
+    if (a.residual && q + 1 < kPasses) load_res(q + 1);
+#pragma unroll
+    for (int p = 0; p < kNC; ++p) {
+      const int r = r0 + p * (kThreads / kCV);
+      const int tr = tile_row(q, r);
+      const v4f p0 = *reinterpret_cast<const v4f*>(lds + r * (C::kBN * 4) + (((2 * c) ^ (r & 15)) << 4));
+      const v4f p1 = *reinterpret_cast<const v4f*>(lds + r * (C::kBN * 4) + (((2 * c + 1) ^ (r & 15)) << 4));
+      const float xsc = s_xs[tr];
+      float v[8] = {p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * xsc * wsc[e];
+      if (a.bias_kind != kBiasNone) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += bias[e];
+      }
+      fused_values<8>(a, v, cur[p]);
+      const int row = m0 + tr;
+      if (row < row_end && left > 0) {
+        const size_t off = (size_t)row * a.n + col;
+        if (a.out_scale) {
+          store_fp8_out<8>(static_cast<uint8_t*>(a.out) + off, v, r_out, a.out_fmt, vec, left);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{v[2 * e], v[2 * e + 1]}), bf2v));
+          uint16_t* dst = static_cast<uint16_t*>(a.out) + off;
+          if (vec) {
+            __builtin_nontemporal_store(hq_u4v{w[0], w[1], w[2], w[3]}, reinterpret_cast<hq_u4v*>(dst));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < left) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+    }
+    __syncthreads();  // the next pass overwrites the rows
+  }
+}
+
 // KTAIL: K is not a multiple of 128, so the A chunks past K are zeroed on their
 // way to LDS; without it the K loop has no masking at all.
 // BSZ > 0: the block-scaled form with blocks of BSZ (32, 64 or 128) along K:
@@ -223,11 +347,7 @@ struct BsCfg {
 // through LDS and the first runs the epilogue. For launches of one tile per CU
 // this puts two wavefronts on each SIMD, so one's loads hide behind the
 // other's MFMAs. Both groups pass the same barriers: K is a multiple of 256.
-// EPI: the fused epilogue. The activation and the residual's addition follow
-// the bias on the float32 values. The tile's residual is loaded whole before
-// the first output is formed (the B fragments' registers are free by then), so
-// its latency is paid once, and every value is in registers before anything is
-// stored: `out` may be the residual's own buffer.
+// EPI: the fused epilogue (above) in place of the plain one.
 template <int XF, int WF, int BM, int TN, int WM, bool KTAIL, int BSZ, bool STRICT = false, int KS = 1, bool EPI = false>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m0, int row_end, int n0,
                                           const uint8_t* __restrict__ wq, const float* __restrict__ ws) {
@@ -530,6 +650,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
 #undef HQ_STEP
 #undef HQ_FOLD
 
+  if constexpr (EPI) {
+    fused_epilogue<C, WM, KS>(a, lds, acc, m0, row_end, n0, tid_all, s_xs, s_ws, s_bias);
+    return;
+  }
+
   // Epilogue: fragment pair (2*jp, 2*jp+1) gives lane l the 8 consecutive output
   // columns n0 + wave*TN + 32*jp + 8*(l/16) .. +7 of row m0 + 16*i + l%16.
   // Scale in fp32 (plus the bias), then either round to bf16
@@ -556,16 +681,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
   for (int jp = 0; jp < C::kIN / 2; ++jp)
 #pragma unroll
     for (int e = 0; e < 8; ++e) wsc[jp][e] = BSF ? 1.0f : s_ws[wave * TN + 32 * jp + ccol + e];
-  uint4 res[EPI ? C::kIM : 1][C::kIN / 2];
-  if constexpr (EPI) {
-    if (a.residual && (KS == 1 || ks == 0)) {
-#pragma unroll
-      for (int i = 0; i < C::kIM; ++i)
-#pragma unroll
-        for (int jp = 0; jp < C::kIN / 2; ++jp)
-          res[i][jp] = residual_cols<8>(a, m0 + wrow * C::kWR + i * 16 + (lane & 15), row_end, n0 + wave * TN + 32 * jp + ccol);
-    }
-  }
   // FP8 output codes of the 256 x 256 tile: the 64 KB code tile fits the two
   // A stages (free once the K loop has ended on its barrier), so it is staged
   // there (8-byte pieces, 16-byte chunks at chunk ^ (row % 16)) and stored as
@@ -590,7 +705,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += s_bias[wave * TN + 32 * jp + ccol + e];
           }
-          if constexpr (EPI) fused_values<8>(a, v, res[i][jp]);
           uint32_t w[2];
           fp8_out_codes<8>(v, r_out, a.out_fmt, w);
           const int cb = wave * TN + 32 * jp + ccol;  // byte column in the tile row
@@ -635,7 +749,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += s_bias[wave * TN + ccol + e];
         }
-        if constexpr (EPI) fused_values<8>(a, v, res[i][0]);
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -677,7 +790,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += s_bias[wave * TN + 32 * jp + ccol + e];
           }
-          if constexpr (EPI) fused_values<8>(a, v, res[i][jp]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const f2v pr = {v[2 * e], v[2 * e + 1]};
@@ -716,7 +828,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, uint8_t* lds, int m
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += s_bias[wave * TN + 32 * jp + ccol + e];
       }
-      if constexpr (EPI) fused_values<8>(a, v, res[i][jp]);
       const size_t off = (size_t)row * a.n + col0;
       const bool full = vec_ok && col0 + 8 <= a.n;
       if (a.out_scale) {
@@ -930,7 +1041,7 @@ __global__ __launch_bounds__(TPB) void gemm_skinny_kernel(GemmArgs a, int splits
   auto load_residual = [&](int f, int i) {
     if constexpr (EPI) {
       const int nb = nb0 + f;
-      if (a.residual) res_r = residual_cols<4>(a, i * 16 + xr, a.m, 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1));
+      if (a.residual) res_r = residual4(a, i * 16 + xr, 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1));
     }
   };
   auto epilogue = [&](int f, int i, v4f t) {
