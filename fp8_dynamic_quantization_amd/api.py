@@ -1,8 +1,10 @@
 """Thin torch-facing binding of libhq: the same entry points as include/hq.h.
 
 Each function only marshals arguments (tensor -> pointer, current HIP stream,
-optional output allocation with ``torch.empty``) and calls the C ABI; every
-step of the computation runs in the library's HIP kernels. With ``stream=``
+optional output allocation with ``torch.empty``) and calls the C ABI, through
+ctypes or, for the operators around the GEMM, through the native module of
+csrc/torch_binding.cpp; every step of the computation runs in the library's HIP
+kernels. With ``stream=``
 every buffer the binding allocates (outputs, zero-filled workspaces) is made
 and filled on that stream, so the launch is ordered after it. Errors come back as
 ``HQInvalidArgument`` (ValueError), ``HQUnsupportedDevice``
@@ -10,7 +12,6 @@ and filled on that stream, so the launch is ordered after it. Errors come back a
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 from typing import NamedTuple
@@ -18,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import (HQ_ACT_NONE, HQ_BF16, HQ_BIAS_BF16, HQ_E4M3, HQ_E5M2, HQ_F32, HQ_PER_CHANNEL, HQ_PER_TENSOR,
-                   HQ_PER_TOKEN, check, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_ring, load)
+                   HQ_PER_TOKEN, check, hq_epilogue, hq_ring, load)
 
 __all__ = [
     "Ring", "hq_scale_count", "hq_quantize_workspace_bytes", "hq_preshuffled_bytes",
@@ -42,8 +43,9 @@ def _on_stream(fn):
     so the binding's allocations and fills are ordered before the launch."""
     @functools.wraps(fn)
     def wrapped(*args, stream=None, **kwargs):
-        ctx = torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
-        with ctx:
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
             return fn(*args, stream=stream, **kwargs)
     return wrapped
 
@@ -563,76 +565,25 @@ class RmsNormQuantized(NamedTuple):
     checkpoint: Checkpoint | None
 
 
-def _real2d(x, name):
-    if x.dtype not in _XT:
-        raise ValueError(f"{name} must be float32 or bfloat16, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be 2-D [rows, cols]")
-    return x.contiguous()
+_NATIVE = None
 
 
-def _like(t, shape, dtype, name):
-    """`t` contiguous (None stays None), checked to be of this shape and type."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t.contiguous()
+def _native():
+    """The native binding module (csrc/torch_binding.cpp), loaded after libhq."""
+    global _NATIVE
+    if _NATIVE is None:
+        load()
+        from . import _hqtorch
+        _hqtorch.setup(check, gemm_workspace)
+        _NATIVE = _hqtorch
+    return _NATIVE
 
 
-def _out(t, shape, dtype, device, name):
-    """The caller's output buffer, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _checkpoint_in(c, rows, cols):
-    q = _like(c.q, (rows, cols), torch.uint8, "checkpoint.q")
-    bs = int(c.block_size)
-    s = _like(c.scales, (rows, -(-cols // bs) if bs > 0 else 0), torch.float32, "checkpoint.scales")
-    return Checkpoint(q, s, bs)
-
-
-def _checkpoint_out(c, rows, cols, device):
-    """None or 0: none; a block size: new buffers; a Checkpoint: its buffers."""
-    if c is None or c is False or (isinstance(c, int) and c == 0):
-        return None
+def _checkpoint_args(c):
+    """(q, scales, block_size) of None or 0 (none), a block size (new buffers) or a Checkpoint (its buffers)."""
     if isinstance(c, Checkpoint):
-        bs = int(c.block_size)
-        nb = -(-cols // bs) if bs > 0 else 0
-        return Checkpoint(_out(c.q, (rows, cols), torch.uint8, device, "checkpoint.q"),
-                          _out(c.scales, (rows, nb), torch.float32, device, "checkpoint.scales"), bs)
-    bs = int(c)
-    nb = -(-cols // bs) if bs > 0 else 0
-    return Checkpoint(torch.empty((rows, cols), dtype=torch.uint8, device=device),
-                      torch.empty((rows, nb), dtype=torch.float32, device=device), bs)
-
-
-def _checkpoint_c(c):
-    return None if c is None else ctypes.byref(hq_checkpoint(c.q.data_ptr(), c.scales.data_ptr(), c.block_size))
-
-
-_SUM_WORKSPACE = {}
-
-
-def _sum_workspace(device, nbytes):
-    """Scratch for the sums over rows, one per device and stream, kept for
-    reuse. It needs no initial value, and launches on one stream are ordered."""
-    if nbytes <= 0:
-        return None
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    ws = _SUM_WORKSPACE.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _SUM_WORKSPACE[key] = ws
-    return ws
+        return c
+    return (None, None, int(c)) if c else (None, None, 0)
 
 
 @_on_stream
@@ -643,23 +594,11 @@ def hq_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor | None, eps: f
     quantized per token. `h`: None (a new buffer when a residual is given), False
     (not written) or a buffer, which may be x or residual itself. `checkpoint`: a
     block size or a Checkpoint whose buffers receive h in 8 bits."""
-    x = _real2d(x, "x")
-    rows, cols = x.shape
-    dev, dt = x.device, x.dtype
-    residual = _like(residual, x.shape, dt, "residual")
-    weight = _like(weight, (cols,), dt, "weight")
-    if h is False or (h is None and residual is None):
-        h = None
-    else:
-        h = _out(h, x.shape, dt, dev, "h")
-    q = _out(q, x.shape, torch.uint8, dev, "q")
-    scale_out = _out(scale_out, (rows,), torch.float32, dev, "scale_out")
-    rstd_out = _out(rstd_out, (rows,), torch.float32, dev, "rstd_out")
-    ckpt = _checkpoint_out(checkpoint, rows, cols, dev)
-    check(load().hq_rmsnorm_quantize_fp8(x.data_ptr(), _addr(residual), _addr(weight), _XT[dt], rows, cols, eps, fmt,
-                                         q.data_ptr(), scale_out.data_ptr(), _addr(h), rstd_out.data_ptr(),
-                                         _checkpoint_c(ckpt), _stream(dev, stream)))
-    return RmsNormQuantized(q, scale_out, h, rstd_out, ckpt)
+    write_h = h is not False and not (h is None and residual is None)
+    cq, cs, bs = _checkpoint_args(checkpoint)
+    q, s, h, r, cq, cs = _native().rmsnorm_quantize(x, weight, eps, fmt, residual, h if write_h else None, write_h, cq,
+                                                    cs, bs, q, scale_out, rstd_out)
+    return RmsNormQuantized(q, s, h, r, Checkpoint(cq, cs, bs) if bs else None)
 
 
 def hq_rmsnorm_backward_workspace_bytes(xt: int, rows: int, cols: int) -> int:
@@ -671,28 +610,12 @@ def hq_rmsnorm_backward(dy: torch.Tensor, h, weight: torch.Tensor | None, rstd: 
                         dresidual: torch.Tensor | None = None, dx=None, dweight=None, workspace=None, stream=None):
     """Backward pass of hq_rmsnorm_quantize_fp8: returns (dx of dy's type, dweight
     float32 [cols]). `h` is the normed tensor in dy's type or its Checkpoint;
-    `dresidual` is added to dx; `dweight` False leaves it out (None returned)."""
-    dy = _real2d(dy, "dy")
-    rows, cols = dy.shape
-    dev, dt = dy.device, dy.dtype
-    ckpt = None
-    if isinstance(h, Checkpoint):
-        ckpt, h = _checkpoint_in(h, rows, cols), None
-    else:
-        h = _like(h, dy.shape, dt, "h")
-    weight = _like(weight, (cols,), dt, "weight")
-    rstd = _like(rstd, (rows,), torch.float32, "rstd")
-    dresidual = _like(dresidual, dy.shape, dt, "dresidual")
-    dx = _out(dx, dy.shape, dt, dev, "dx")
-    dweight = None if dweight is False else _out(dweight, (cols,), torch.float32, dev, "dweight")
-    lib = load()
-    if workspace is None and dweight is not None:
-        workspace = _sum_workspace(dev, int(lib.hq_rmsnorm_backward_workspace_bytes(_XT[dt], rows, cols)))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(lib.hq_rmsnorm_backward(dy.data_ptr(), _addr(h), _checkpoint_c(ckpt), _addr(weight), rstd.data_ptr(),
-                                  _addr(dresidual), _XT[dt], rows, cols, dx.data_ptr(), _addr(dweight), _addr(workspace),
-                                  ws_bytes, _stream(dev, stream)))
-    return dx, dweight
+    `dresidual` is added to dx, which may be dy or dresidual itself; `dweight` False
+    leaves the sum over rows out (None returned)."""
+    cq, cs, bs, h = (*h, None) if isinstance(h, Checkpoint) else (None, None, 0, h)
+    want = dweight is not False
+    return _native().rmsnorm_backward(dy, h, cq, cs, bs, weight, rstd, dresidual, dx, dweight if want else None, want,
+                                      workspace)
 
 
 @_on_stream
@@ -702,28 +625,10 @@ def hq_gemm_a8w8_fused(xq: torch.Tensor, xf: int, wq_pre: torch.Tensor, wf: int,
                        residual: torch.Tensor | None = None, out_scale: torch.Tensor | None = None,
                        out_fmt: int = HQ_E4M3, out=None, workspace=None, stream=None) -> torch.Tensor:
     """hq_gemm_a8w8_epilogue with act(v + bias) and a bf16 residual [m, n] added
-    after it. `out` (bf16) may be the residual itself. Returns out."""
-    xq, x_scale, w_scale = xq.contiguous(), x_scale.contiguous(), w_scale.contiguous()
-    m, k = xq.shape
-    dev = xq.device
-    if bias is not None:
-        if bias.numel() != n or (bias_type == HQ_BIAS_BF16 and bias.dtype != torch.bfloat16):
-            raise ValueError("bias must have n elements, bf16 unless bias_type says FP8 codes")
-        bias = bias.contiguous()
-    residual = _like(residual, (m, n), torch.bfloat16, "residual")
-    out = _out(out, (m, n), torch.bfloat16 if out_scale is None else torch.uint8, dev, "out")
-    lib = load()
-    if workspace is None:
-        workspace = gemm_workspace(dev, int(lib.hq_gemm_workspace_bytes(m, n, k)))
-    elif workspace is False:
-        workspace = None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    ep = hq_fused_epilogue(_addr(bias), int(bias_type), _addr(bias_scale), _addr(out_scale), int(out_fmt), int(act),
-                           _addr(residual))
-    check(lib.hq_gemm_a8w8_fused(xq.data_ptr(), xf, wq_pre.data_ptr(), wf, x_scale.data_ptr(), x_scale.numel(),
-                                 w_scale.data_ptr(), w_scale.numel(), m, n, k, ctypes.byref(ep), out.data_ptr(),
-                                 _addr(workspace), ws_bytes, _stream(dev, stream)))
-    return out
+    after it. `out` (bf16) may be the residual itself. `workspace` as in
+    hq_gemm_a8w8. Returns out."""
+    return _native().gemm_fused(xq, xf, wq_pre, wf, x_scale, w_scale, n, bias, bias_type, bias_scale, act, residual,
+                                out_scale, out_fmt, out, workspace)
 
 
 @_on_stream
@@ -732,18 +637,9 @@ def hq_act_quantize_fp8(z: torch.Tensor, act: int, fmt: int = HQ_E4M3, *, gated:
     """act(z), or gated act(z[:, :cols]) * z[:, cols:], quantized per token: returns
     (q uint8 [rows, cols], scale float32 [rows], Checkpoint of z or None).
     `checkpoint`: a block size or a Checkpoint whose buffers receive z in 8 bits."""
-    z = _real2d(z, "z")
-    rows, wide = z.shape
-    if gated and wide % 2:
-        raise ValueError("a gated z has an even number of columns")
-    cols = wide // 2 if gated else wide
-    dev = z.device
-    q = _out(q, (rows, cols), torch.uint8, dev, "q")
-    scale_out = _out(scale_out, (rows,), torch.float32, dev, "scale_out")
-    ckpt = _checkpoint_out(checkpoint, rows, wide, dev)
-    check(load().hq_act_quantize_fp8(z.data_ptr(), _XT[z.dtype], rows, cols, act, int(gated), fmt, q.data_ptr(),
-                                     scale_out.data_ptr(), _checkpoint_c(ckpt), _stream(dev, stream)))
-    return q, scale_out, ckpt
+    cq, cs, bs = _checkpoint_args(checkpoint)
+    q, s, cq, cs = _native().act_quantize(z, act, fmt, bool(gated), cq, cs, bs, q, scale_out)
+    return q, s, Checkpoint(cq, cs, bs) if bs else None
 
 
 def hq_act_backward_workspace_bytes(xt: int, rows: int, cols: int, gated: bool) -> int:
@@ -756,20 +652,9 @@ def hq_act_backward(da: torch.Tensor, z: Checkpoint, act: int, *, gated: bool = 
     """Backward pass of hq_act_quantize_fp8 from z's checkpoint: returns (dz of da's
     type and z's shape, dbias float32 of z's width); `dbias` False leaves the sum
     over rows out (None returned)."""
-    da = _real2d(da, "da")
-    rows, cols = da.shape
-    wide = 2 * cols if gated else cols
-    dev, dt = da.device, da.dtype
-    z = _checkpoint_in(z, rows, wide)
-    dz = _out(dz, (rows, wide), dt, dev, "dz")
-    dbias = None if dbias is False else _out(dbias, (wide,), torch.float32, dev, "dbias")
-    lib = load()
-    if workspace is None and dbias is not None:
-        workspace = _sum_workspace(dev, int(lib.hq_act_backward_workspace_bytes(_XT[dt], rows, cols, int(gated))))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(lib.hq_act_backward(da.data_ptr(), _checkpoint_c(z), _XT[dt], rows, cols, act, int(gated), dz.data_ptr(),
-                              _addr(dbias), _addr(workspace), ws_bytes, _stream(dev, stream)))
-    return dz, dbias
+    want = dbias is not False
+    return _native().act_backward(da, z.q, z.scales, z.block_size, act, bool(gated), dz, dbias if want else None, want,
+                                  workspace)
 
 
 def hq_wgrad_workspace_bytes(m: int, n: int, k: int, dwt: int) -> int:
@@ -782,29 +667,8 @@ def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tenso
     """dw[n, k] = base + sum_m g[m, n] x_scale[m] dec(xq[m, k]) from a bf16 gradient
     g [m, n] and the codes xq [m, k] that the forward GEMM read; dw of `dtype`
     (bfloat16 or float32; a float32 base only with float32, and dw may be base).
-    `workspace`: None (a shared buffer of the size the shape wants), False (none) or
-    a uint8 tensor."""
-    if g.dim() != 2 or g.dtype != torch.bfloat16:
-        raise ValueError("g must be a 2-D bfloat16 tensor [m, n]")
+    `workspace`: None (allocated where the shape wants one), False (none) or a uint8
+    tensor."""
     if dtype not in _XT:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
-    g = g.contiguous()
-    m, n = g.shape
-    if xq.dim() != 2 or xq.shape[0] != m or xq.dtype != torch.uint8:
-        raise ValueError("xq must be uint8 codes [m, k]")
-    if x_scale.dtype != torch.float32:
-        raise ValueError("x_scale must be float32")
-    xq, x_scale = xq.contiguous(), x_scale.contiguous()
-    k = xq.shape[1]
-    dev = g.device
-    base = _like(base, (n, k), torch.float32, "base")
-    dw = _out(dw, (n, k), dtype, dev, "dw")
-    lib = load()
-    if workspace is None:
-        workspace = _sum_workspace(dev, int(lib.hq_wgrad_workspace_bytes(m, n, k, _XT[dtype])))
-    elif workspace is False:
-        workspace = None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(lib.hq_wgrad_a8(g.data_ptr(), xq.data_ptr(), xf, x_scale.data_ptr(), x_scale.numel(), m, n, k, _addr(base),
-                          dw.data_ptr(), _XT[dtype], _addr(workspace), ws_bytes, _stream(dev, stream)))
-    return dw
+    return _native().wgrad(g, xq, xf, x_scale, _XT[dtype], base, dw, workspace)

@@ -1,4 +1,5 @@
-"""Build libhq.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libhq.so (the C-ABI library) for gfx950 with hipcc, in-tree, and the
+native torch binding _hqtorch.so (host code only) beside it.
 
     python -m fp8_dynamic_quantization_amd.build
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhq.so")
+BINDING = os.path.join(PKG, "_hqtorch.so")
 
 SOURCES = ["quantize.hip", "gemm.hip", "gemm_fused.hip", "blockscaled.hip", "norm.hip", "act.hip", "wgrad.hip", "probe.hip",
            "hq_api.cpp"]
@@ -48,17 +50,45 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source and link libhq.so; returns the library path."""
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
+def _compile_binding() -> str:
+    """The binding's object: a CPython module against torch's C++ headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD, "torch_binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-fPIC", "-std=c++17", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-I", INCLUDE, *(f"-isystem{p}" for p in cpp_extension.include_paths()), "-isystem/opt/rocm/include",
+           f"-isystem{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "torch_binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        raise RuntimeError(f"compiling torch_binding.cpp failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link(cmd: list[str], out: str) -> None:
+    r = subprocess.run([*cmd, "-o", out + ".tmp"], capture_output=True, text=True)
+    if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    os.replace(out + ".tmp", out)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source and link libhq.so and the binding; returns the library path."""
+    from torch.utils import cpp_extension
+
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
+        objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
+    _link([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libhq.so", *objs], LIB)
+    # torch's libraries are in the process already when the binding is imported
+    torch_lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
+    _link([os.environ.get("CXX", "g++"), "-shared", binding, f"-L{PKG}", "-l:libhq.so", f"-L{torch_lib}", "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], BINDING)
     if verbose:
         print(f"built {LIB}")
     return LIB
