@@ -88,7 +88,7 @@ def build(verbose: bool = False) -> str:
     # torch's libraries are in the process already when the binding is imported
     torch_lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
     _link([os.environ.get("CXX", "g++"), "-shared", binding, f"-L{PKG}", "-l:libhq.so", f"-L{torch_lib}", "-lc10", "-lc10_hip",
-           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], BINDING)
+           "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], BINDING)
     if verbose:
         print(f"built {LIB}")
     return LIB

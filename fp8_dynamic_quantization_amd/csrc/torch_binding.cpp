@@ -11,7 +11,7 @@
 // None stands for a tensor that is not given. Refusals raise ValueError, and
 // errors of the library go through _lib.check.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Device.h>
@@ -63,9 +63,16 @@ Tensor input(Tensor t, at::IntArrayRef shape, ScalarType dt, const Tensor& like,
   return t.contiguous();
 }
 
+// A new tensor on `like`'s GPU, from the caching allocator (torch.empty without
+// its dispatch).
+Tensor fresh(at::IntArrayRef shape, ScalarType dt, const Tensor& like, const char* name) {
+  TORCH_CHECK_VALUE(like.is_cuda(), "tensors must be on the GPU, got ", like.device(), " for ", name);
+  return at::detail::empty_cuda(shape, dt, like.device(), std::nullopt);
+}
+
 // The caller's output buffer, checked, or a new one.
 Tensor output(Tensor t, at::IntArrayRef shape, ScalarType dt, const Tensor& like, const char* name) {
-  if (!t.defined()) return at::empty(shape, like.options().dtype(dt));
+  if (!t.defined()) return fresh(shape, dt, like, name);
   TORCH_CHECK_VALUE(t.scalar_type() == dt && t.sizes() == shape && t.is_contiguous() && t.device() == like.device(), name,
                     " must be contiguous ", dt, " ", shape, " on ", like.device(), ", got ", t.scalar_type(), " ", t.sizes(),
                     " on ", t.device());
@@ -88,7 +95,7 @@ hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.
 // ordered on the current stream, and under graph capture it belongs to the graph.
 Tensor scratch(const Tensor& given, bool allocate, size_t bytes, const Tensor& like) {
   if (given.defined() || !allocate || bytes == 0) return given;
-  return at::empty({(int64_t)bytes}, like.options().dtype(ScalarType::Byte));
+  return fresh({(int64_t)bytes}, ScalarType::Byte, like, "workspace");
 }
 size_t bytes_of(const Tensor& t) { return t.defined() ? t.nbytes() : 0; }
 
