@@ -1188,22 +1188,26 @@ static hipError_t launch_skinny(const GemmArgs& a, void* workspace, size_t works
     }
     hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 1, 1, 4, STRICT, EPI>), grid, block, 0, st, a, p.splits, chunk, halves,
                        counters, partials);
-  } else if (p.mb == 2) {
+    return hipGetLastError();
+  }
+  // (more than 16 rows with the fused epilogue take gemm_rows_kernel)
+  if constexpr (EPI) return hipErrorInvalidValue;
+  else if (p.mb == 2) {
     if constexpr (!STRICT) {
       if (deep2) {
-        hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 2, 2, 4, STRICT, EPI, 256>), grid, block, 0, st, a, p.splits, chunk,
+        hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 2, 2, 4, STRICT, false, 256>), grid, block, 0, st, a, p.splits, chunk,
                            halves, counters, partials);
         return hipGetLastError();
       }
     }
-    hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 2, 2, 2, STRICT, EPI>), grid, block, 0, st, a, p.splits, chunk, halves,
+    hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 2, 2, 2, STRICT, false>), grid, block, 0, st, a, p.splits, chunk, halves,
                        counters, partials);
   } else if constexpr (!STRICT) {
     if (wg_waves <= 4 && bpw > 1)
-      hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 4, 2, 4, STRICT, EPI, 256>), grid, block, 0, st, a, p.splits, chunk,
+      hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 4, 2, 4, STRICT, false, 256>), grid, block, 0, st, a, p.splits, chunk,
                          halves, counters, partials);
     else
-      hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 4, 2, 1, STRICT, EPI>), grid, block, 0, st, a, p.splits, chunk, halves,
+      hipLaunchKernelGGL((gemm_skinny_kernel<XF, WF, 4, 2, 1, STRICT, false>), grid, block, 0, st, a, p.splits, chunk, halves,
                          counters, partials);
   }
   return hipGetLastError();

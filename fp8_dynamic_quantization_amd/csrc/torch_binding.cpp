@@ -234,7 +234,7 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   on_gpu(xq, "xq");
   Tensor work;
   if (a[15] == Py_None) {
-    const int64_t need = hq_gemm_workspace_bytes(m, n, k);
+    const int64_t need = m <= 16 ? hq_gemm_workspace_bytes(m, n, k) : 0;  // more rows use none
     if (need > 0) {
       THPObjectPtr dev(THPDevice_New(xq.device()));
       THPObjectPtr r(PyObject_CallFunction(g_gemm_workspace, "OL", dev.get(), (long long)need));

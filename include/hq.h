@@ -590,7 +590,7 @@ typedef struct hq_fused_epilogue {
  *   out[m, n] = bf16_rne(v), or with out_scale the FP8 code as in
  *               hq_gemm_a8w8_epilogue
  * `ep` is a host pointer and must not be NULL. A bf16 `out` may be the
- * residual's own buffer. All other arguments, the workspace rule and the
+ * residual's own buffer. Only m <= 16 uses a workspace. All other arguments, the workspace rule and the
  * requirements are those of hq_gemm_a8w8_epilogue. */
 hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
                              int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
