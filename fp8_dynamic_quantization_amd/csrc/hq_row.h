@@ -181,4 +181,34 @@ __device__ __forceinline__ void decode_vec(const uint32_t* w, float s, float* f)
   }
 }
 
+// ---- sums over rows in one workgroup ---------------------------------------------
+// A workgroup of 1024 threads holds 8 vector columns (128 bytes of a row) of 128
+// rows at a time: lane l of wavefront w is column l % 8 of row slot 8 w + l / 8.
+// N values per thread are added over the slots in a fixed order; threads 0 .. 7
+// return true with their column's sums in v. `s` holds 16 * 8 * N floats.
+constexpr int kColVecs = 8, kColSlots = 128;
+template <int N>
+__device__ __forceinline__ bool slots_sum(float* v, float* s) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    v[e] += __shfl_xor(v[e], 8, 64);
+    v[e] += __shfl_xor(v[e], 16, 64);
+    v[e] += __shfl_xor(v[e], 32, 64);
+  }
+  if (lane < 8) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[(wave * N + e) * 8 + lane] = v[e];
+  }
+  __syncthreads();
+  if (threadIdx.x >= 8) return false;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    v[e] = s[e * 8 + lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) v[e] += s[(w * N + e) * 8 + lane];
+  }
+  return true;
+}
+
 }  // namespace hq
