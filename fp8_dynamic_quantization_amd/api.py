@@ -579,6 +579,8 @@ def _native():
     return _NATIVE
 
 
+# The functions below open a given stream's context themselves: the wrapper's
+# repacked call costs half a microsecond, a tenth of a small call's host time.
 def _checkpoint_args(c):
     """(q, scales, block_size) of None or 0 (none), a block size (new buffers) or a Checkpoint (its buffers)."""
     if isinstance(c, Checkpoint):
@@ -586,7 +588,6 @@ def _checkpoint_args(c):
     return (None, None, int(c)) if c else (None, None, 0)
 
 
-@_on_stream
 def hq_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, fmt: int = HQ_E4M3, *,
                             residual: torch.Tensor | None = None, h=None, checkpoint=None, q=None, scale_out=None,
                             rstd_out=None, stream=None) -> RmsNormQuantized:
@@ -594,6 +595,10 @@ def hq_rmsnorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor | None, eps: f
     quantized per token. `h`: None (a new buffer when a residual is given), False
     (not written) or a buffer, which may be x or residual itself. `checkpoint`: a
     block size or a Checkpoint whose buffers receive h in 8 bits."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_rmsnorm_quantize_fp8(x, weight, eps, fmt, residual=residual, h=h, checkpoint=checkpoint, q=q,
+                                           scale_out=scale_out, rstd_out=rstd_out)
     write_h = h is not False and not (h is None and residual is None)
     cq, cs, bs = _checkpoint_args(checkpoint)
     q, s, h, r, cq, cs = _native().rmsnorm_quantize(x, weight, eps, fmt, residual, h if write_h else None, write_h, cq,
@@ -605,20 +610,22 @@ def hq_rmsnorm_backward_workspace_bytes(xt: int, rows: int, cols: int) -> int:
     return int(load().hq_rmsnorm_backward_workspace_bytes(xt, rows, cols))
 
 
-@_on_stream
 def hq_rmsnorm_backward(dy: torch.Tensor, h, weight: torch.Tensor | None, rstd: torch.Tensor, *,
                         dresidual: torch.Tensor | None = None, dx=None, dweight=None, workspace=None, stream=None):
     """Backward pass of hq_rmsnorm_quantize_fp8: returns (dx of dy's type, dweight
     float32 [cols]). `h` is the normed tensor in dy's type or its Checkpoint;
     `dresidual` is added to dx, which may be dy or dresidual itself; `dweight` False
     leaves the sum over rows out (None returned)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_rmsnorm_backward(dy, h, weight, rstd, dresidual=dresidual, dx=dx, dweight=dweight,
+                                       workspace=workspace)
     cq, cs, bs, h = (*h, None) if isinstance(h, Checkpoint) else (None, None, 0, h)
     want = dweight is not False
     return _native().rmsnorm_backward(dy, h, cq, cs, bs, weight, rstd, dresidual, dx, dweight if want else None, want,
                                       workspace)
 
 
-@_on_stream
 def hq_gemm_a8w8_fused(xq: torch.Tensor, xf: int, wq_pre: torch.Tensor, wf: int, x_scale: torch.Tensor,
                        w_scale: torch.Tensor, n: int, *, bias: torch.Tensor | None = None,
                        bias_type: int = HQ_BIAS_BF16, bias_scale: torch.Tensor | None = None, act: int = HQ_ACT_NONE,
@@ -627,16 +634,23 @@ def hq_gemm_a8w8_fused(xq: torch.Tensor, xf: int, wq_pre: torch.Tensor, wf: int,
     """hq_gemm_a8w8_epilogue with act(v + bias) and a bf16 residual [m, n] added
     after it. `out` (bf16) may be the residual itself. `workspace` as in
     hq_gemm_a8w8. Returns out."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_gemm_a8w8_fused(xq, xf, wq_pre, wf, x_scale, w_scale, n, bias=bias, bias_type=bias_type,
+                                      bias_scale=bias_scale, act=act, residual=residual, out_scale=out_scale,
+                                      out_fmt=out_fmt, out=out, workspace=workspace)
     return _native().gemm_fused(xq, xf, wq_pre, wf, x_scale, w_scale, n, bias, bias_type, bias_scale, act, residual,
                                 out_scale, out_fmt, out, workspace)
 
 
-@_on_stream
 def hq_act_quantize_fp8(z: torch.Tensor, act: int, fmt: int = HQ_E4M3, *, gated: bool = False, checkpoint=None, q=None,
                         scale_out=None, stream=None):
     """act(z), or gated act(z[:, :cols]) * z[:, cols:], quantized per token: returns
     (q uint8 [rows, cols], scale float32 [rows], Checkpoint of z or None).
     `checkpoint`: a block size or a Checkpoint whose buffers receive z in 8 bits."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_act_quantize_fp8(z, act, fmt, gated=gated, checkpoint=checkpoint, q=q, scale_out=scale_out)
     cq, cs, bs = _checkpoint_args(checkpoint)
     q, s, cq, cs = _native().act_quantize(z, act, fmt, bool(gated), cq, cs, bs, q, scale_out)
     return q, s, Checkpoint(cq, cs, bs) if bs else None
@@ -646,12 +660,14 @@ def hq_act_backward_workspace_bytes(xt: int, rows: int, cols: int, gated: bool) 
     return int(load().hq_act_backward_workspace_bytes(xt, rows, cols, int(gated)))
 
 
-@_on_stream
 def hq_act_backward(da: torch.Tensor, z: Checkpoint, act: int, *, gated: bool = False, dz=None, dbias=None,
                     workspace=None, stream=None):
     """Backward pass of hq_act_quantize_fp8 from z's checkpoint: returns (dz of da's
     type and z's shape, dbias float32 of z's width); `dbias` False leaves the sum
     over rows out (None returned)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_act_backward(da, z, act, gated=gated, dz=dz, dbias=dbias, workspace=workspace)
     want = dbias is not False
     return _native().act_backward(da, z.q, z.scales, z.block_size, act, bool(gated), dz, dbias if want else None, want,
                                   workspace)
@@ -661,7 +677,6 @@ def hq_wgrad_workspace_bytes(m: int, n: int, k: int, dwt: int) -> int:
     return int(load().hq_wgrad_workspace_bytes(m, n, k, dwt))
 
 
-@_on_stream
 def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
                 base: torch.Tensor | None = None, dw=None, workspace=None, stream=None) -> torch.Tensor:
     """dw[n, k] = base + sum_m g[m, n] x_scale[m] dec(xq[m, k]) from a bf16 gradient
@@ -669,6 +684,9 @@ def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tenso
     (bfloat16 or float32; a float32 base only with float32, and dw may be base).
     `workspace`: None (allocated where the shape wants one), False (none) or a uint8
     tensor."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_wgrad_a8(g, xq, xf, x_scale, dtype=dtype, base=base, dw=dw, workspace=workspace)
     if dtype not in _XT:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     return _native().wgrad(g, xq, xf, x_scale, _XT[dtype], base, dw, workspace)
