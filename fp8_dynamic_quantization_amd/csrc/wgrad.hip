@@ -103,53 +103,8 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   const int g_dst = g_r * C::kGRow + (((g_c >> 1) ^ (g_r & 7)) << 5) + ((g_c & 1) << 4);
   const int x_dst = x_r * C::kXRow + ((x_c ^ x_swizzle<BK>(x_r)) << 4);
   const __amdgpu_buffer_rsrc_t s_rsrc = row_rsrc(a.x_scale, a.x_scale_per_row ? (uint32_t)a.m * 4u : 4u);
-
-  uint4 rg[C::kGVec], rx[C::kXVec];
-  float rs[C::kGVec];
-  // Tokens past m read zeros (past the extents), and so do columns past n and k.
-  auto load = [&](int s) {
-    const int64_t m0 = (int64_t)s * MS;
-    const uint32_t rows = s < s_end ? (uint32_t)min((int64_t)MS, a.m - m0) : 0u;
-    const __amdgpu_buffer_rsrc_t g_rsrc =
-        row_rsrc(a.g + (size_t)(rows ? m0 : 0) * a.n + n0, rows ? rows * (uint32_t)a.n * 2u - (uint32_t)n0 * 2u : 0u);
-    const __amdgpu_buffer_rsrc_t x_rsrc =
-        row_rsrc(a.xq + (size_t)(rows ? m0 : 0) * a.k + k0, rows ? rows * (uint32_t)a.k - (uint32_t)k0 : 0u);
-#pragma unroll
-    for (int v = 0; v < C::kGVec; ++v)
-      rg[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(g_rsrc, g_vo, (int)((uint32_t)(v * C::kGStep) * (uint32_t)a.n * 2u), 0));
-#pragma unroll
-    for (int v = 0; v < C::kXVec; ++v)
-      rx[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_vo, (int)((uint32_t)(v * C::kXStep) * (uint32_t)a.k), 0));
-#pragma unroll
-    for (int v = 0; v < C::kGVec; ++v)
-      rs[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          s_rsrc, !rows ? kBadOffset : a.x_scale_per_row ? ((int)m0 + v * C::kGStep + g_r) * 4 : 0, 0, 0));
-  };
-  uint8_t* const lds_g = lds + ks * 2 * C::kStage;
-  auto store = [&](int buf) {
-    uint8_t* g = lds_g + buf * C::kStage;
-    uint8_t* x = g + C::kGBytes * (HILO ? 2 : 1);
-#pragma unroll
-    for (int v = 0; v < C::kGVec; ++v) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
-        hi[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2v));
-        if constexpr (HILO) {
-          // an infinite or NaN hi carries the value alone
-          const float h0 = bf16_lo(hi[e]), h1 = bf16_hi(hi[e]);
-          const f2v q = {fabsf(h0) < __builtin_inff() ? p[0] - h0 : 0.0f, fabsf(h1) < __builtin_inff() ? p[1] - h1 : 0.0f};
-          lo[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2v));
-        }
-      }
-      *reinterpret_cast<uint4*>(g + g_dst + v * C::kGStep * C::kGRow) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if constexpr (HILO)
-        *reinterpret_cast<uint4*>(g + C::kGBytes + g_dst + v * C::kGStep * C::kGRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-#pragma unroll
-    for (int v = 0; v < C::kXVec; ++v) *reinterpret_cast<uint4*>(x + x_dst + v * C::kXStep * C::kXRow) = rx[v];
-  };
+  const int s_step = a.x_scale_per_row ? 4 : 0;  // bytes from a token's scale to the next one's
+  constexpr int H = HILO ? 2 : 1;
 
   // Operand reads. The swizzle only touches address bits below the row, and a
   // fragment's number only bits of the unit, so a fragment's address is the
@@ -159,6 +114,56 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   const int g_rd = g_row * C::kGRow + (((wn * C::FN) ^ (l16 >> 2)) << 5) + ((l16 & 3) << 3);
   const int x_row = 8 * grp + (l16 >> 1);
   const int x_rd = x_row * C::kXRow + (((wk * C::FK) ^ x_swizzle<BK>(x_row)) << 4) + ((l16 & 1) << 3);
+  uint8_t* const lds_g = lds + ks * 2 * C::kStage;
+  constexpr int kXOff = C::kGBytes * H;  // X after G in a stage
+
+  // Loads: step s as range-checked buffers whose rows past m, and columns past n
+  // and k, read zero. Piece v of G comes with its token's scale.
+  uint4 rg[C::kGVec], rx[C::kXVec];
+  float rs[C::kGVec];
+  __amdgpu_buffer_rsrc_t g_rsrc, x_rsrc;
+  int s_vo;  // byte offset of the scale of the thread's first row; past the extent where the step has no rows
+  auto set_step = [&](int s) {
+    const int64_t m0 = (int64_t)s * MS;
+    const uint32_t rows = s < s_end ? (uint32_t)min((int64_t)MS, a.m - m0) : 0u;
+    g_rsrc = row_rsrc(a.g + (size_t)(rows ? m0 : 0) * a.n + n0, rows ? rows * (uint32_t)a.n * 2u - (uint32_t)n0 * 2u : 0u);
+    x_rsrc = row_rsrc(a.xq + (size_t)(rows ? m0 : 0) * a.k + k0, rows ? rows * (uint32_t)a.k - (uint32_t)k0 : 0u);
+    s_vo = rows ? ((int)m0 + g_r) * s_step : kBadOffset;
+  };
+  auto load_g = [&](int v) {
+    rg[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(g_rsrc, g_vo, (int)((uint32_t)(v * C::kGStep) * (uint32_t)a.n * 2u), 0));
+    rs[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_vo, v * C::kGStep * s_step, 0));
+  };
+  auto load_x = [&](int v) {
+    rx[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_vo, (int)((uint32_t)(v * C::kXStep) * (uint32_t)a.k), 0));
+  };
+  auto store_g = [&](uint8_t* stage, int v) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
+      hi[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2v));
+      if constexpr (HILO) {
+        const f2v q = {p[0] - bf16_lo(hi[e]), p[1] - bf16_hi(hi[e])};
+        lo[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2v));
+      }
+    }
+    const uint4 hv = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(stage + g_dst + v * C::kGStep * C::kGRow) = hv;
+    if constexpr (HILO) {
+      if (__any(vec_absmax_raw<kBF16>(hv) >= kInfBits)) {  // rare: an infinite or NaN hi carries the value alone
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((hi[e] & 0x7f80u) == 0x7f80u) lo[e] &= 0xffff0000u;
+          if ((hi[e] & 0x7f800000u) == 0x7f800000u) lo[e] &= 0xffffu;
+        }
+      }
+      *reinterpret_cast<uint4*>(stage + C::kGBytes + g_dst + v * C::kGStep * C::kGRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  };
+  auto store_x = [&](uint8_t* stage, int v) {
+    *reinterpret_cast<uint4*>(stage + kXOff + x_dst + v * C::kXStep * C::kXRow) = rx[v];
+  };
 
   v4f acc[C::FK][C::FN];
 #pragma unroll
@@ -166,31 +171,57 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int buf) {
-    const uint8_t* g = lds_g + buf * C::kStage;
-    const uint8_t* x = g + C::kGBytes * (HILO ? 2 : 1);
+  auto read_g = [&](const uint8_t* stage, int ss, wg_b8 (&f)[H][C::FN]) {
 #pragma unroll
-    for (int ss = 0; ss < MS / 32; ++ss) {
-      wg_b8 fg[HILO ? 2 : 1][C::FN];
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int h = 0; h < (HILO ? 2 : 1); ++h)
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          const wg_s4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (HQ_LDS wg_s4*)(g + h * C::kGBytes + (g_rd ^ (j << 5)) + ss * 32 * C::kGRow));
-          const wg_s4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (HQ_LDS wg_s4*)(g + h * C::kGBytes + (g_rd ^ (j << 5) ^ (4 << 5)) + (ss * 32 + 4) * C::kGRow));
-          fg[h][j] = __builtin_bit_cast(wg_b8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-#pragma unroll
-      for (int i = 0; i < C::FK; ++i) {
-        const wg_i2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((HQ_LDS wg_i2*)(x + (x_rd ^ (i << 4)) + ss * 32 * C::kXRow));
-        const wg_b8 fx = bf16x8<XF>(c);
-#pragma unroll
-        for (int h = 0; h < (HILO ? 2 : 1); ++h)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fg[h][j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < C::FN; ++j) {
+        const wg_s4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5)) + ss * 32 * C::kGRow));
+        const wg_s4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5) ^ (4 << 5)) + (ss * 32 + 4) * C::kGRow));
+        f[h][j] = __builtin_bit_cast(wg_b8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
       }
+  };
+  auto read_x = [&](const uint8_t* stage, int slot) -> wg_i2 {
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (HQ_LDS wg_i2*)(stage + kXOff + (x_rd ^ ((slot % C::FK) << 4)) + (slot / C::FK) * 32 * C::kXRow));
+  };
+
+  // One step of MS tokens as slots of one X fragment each: the next slot's
+  // fragment is read, one staging piece of the next step is converted, stored to
+  // the other stage and replaced by its load for the step after, and the slot's
+  // MFMAs run, so conversions and LDS traffic lie between matrix instructions
+  // instead of before them (2048 x 4096 x 1024: 27.0 us with all staging ahead of
+  // the step's MFMAs). The barriers keep the compiler from gathering them again.
+  constexpr int kSub = MS / 32, kSlots = kSub * C::FK, kPieces = C::kGVec + C::kXVec;
+  static_assert(kPieces <= kSlots, "at most one staging piece per slot");
+  auto step = [&](int buf) {
+    const uint8_t* cur = lds_g + buf * C::kStage;
+    uint8_t* nxt = lds_g + (buf ^ 1) * C::kStage;
+    wg_b8 fg[kSub > 1 ? 2 : 1][H][C::FN];
+    wg_i2 fx[2];
+    read_g(cur, 0, fg[0]);
+    fx[0] = read_x(cur, 0);
+#pragma unroll
+    for (int sl = 0; sl < kSlots; ++sl) {
+      const int ss = sl / C::FK, i = sl % C::FK;
+      if (sl + 1 < kSlots) fx[(sl + 1) & 1] = read_x(cur, sl + 1);
+      if (i == C::FK / 2 && ss + 1 < kSub) read_g(cur, ss + 1, fg[(ss + 1) & (kSub > 1 ? 1 : 0)]);
+      const wg_b8 x = bf16x8<XF>(fx[sl & 1]);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, fg[ss & (kSub > 1 ? 1 : 0)][h][j], acc[i][j], 0, 0, 0);
+      if (sl < C::kGVec) {
+        store_g(nxt, sl);
+        load_g(sl);
+      } else if (sl < kPieces) {
+        store_x(nxt, sl - C::kGVec);
+        load_x(sl - C::kGVec);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -198,14 +229,23 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   // both groups of KS == 2 pass the same number of barriers (steps past the end
   // hold zeros).
   const int iters = (max(s_end - s_begin, 0) + KS - 1) / KS;
-  load(s_begin + ks);
-  store(0);
-  load(s_begin + ks + KS);
+  auto load_all = [&](int s) {
+    set_step(s);
+#pragma unroll
+    for (int v = 0; v < C::kGVec; ++v) load_g(v);
+#pragma unroll
+    for (int v = 0; v < C::kXVec; ++v) load_x(v);
+  };
+  load_all(s_begin + ks);
+#pragma unroll
+  for (int v = 0; v < C::kGVec; ++v) store_g(lds_g, v);
+#pragma unroll
+  for (int v = 0; v < C::kXVec; ++v) store_x(lds_g, v);
+  load_all(s_begin + ks + KS);
   __syncthreads();
   for (int i = 0; i < iters; ++i) {
-    store((i + 1) & 1);
-    load(s_begin + ks + (i + 2) * KS);
-    compute(i & 1);
+    set_step(s_begin + ks + (i + 2) * KS);
+    step(i & 1);
     __syncthreads();
   }
 
