@@ -47,13 +47,15 @@ struct WgCfg {
   static constexpr int kGStep = T / (BN / 8), kXStep = T / (BK / 16);          // rows between them
   static constexpr int kLds = 2 * KS * kStage;
   static_assert(WN == 64 && (FK == 8 || FK == 4), "the swizzles below assume these");
-  static_assert(kGStep % 8 == 0 && kXStep % 16 == 0, "a thread's pieces share one swizzle");
+  static_assert(kGStep % 16 == 0 && kXStep % 16 == 0, "a thread's pieces share one swizzle");
   static_assert(KS == 1 || BN * BK * 4 <= kLds, "the second group's sums fit the stages");
 };
 
 // Rows of an LDS tile start on the same bank, so the pieces of a row are permuted
-// by its number: units of 32 bytes of a G row (what a transpose read takes of one
-// row) by row % 8, units of 16 bytes of an X row so that 16 rows cover all banks.
+// by its number. A 16-bit transpose read takes units of 32 bytes of the rows r,
+// r + 8, r + 16, r + 24 for four r at a time, an 8-bit one units of 16 bytes of 32
+// rows: with these permutations each half of a read covers 256 bytes of banks once.
+__device__ __forceinline__ int g_swizzle(int row) { return (row & 3) | ((row >> 1) & 4); }
 template <int BK>
 __device__ __forceinline__ int x_swizzle(int row) {
   return BK == 256 ? row & 15 : (row >> 1) & 7;
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   const int x_c = t % (BK / 16), x_r = t / (BK / 16);
   const int g_vo = n0 + g_c * 8 < a.n ? (int)((uint32_t)g_r * (uint32_t)a.n * 2u + (uint32_t)g_c * 16u) : kBadOffset;
   const int x_vo = k0 + x_c * 16 < a.k ? (int)((uint32_t)x_r * (uint32_t)a.k + (uint32_t)x_c * 16u) : kBadOffset;
-  const int g_dst = g_r * C::kGRow + (((g_c >> 1) ^ (g_r & 7)) << 5) + ((g_c & 1) << 4);
+  const int g_dst = g_r * C::kGRow + (((g_c >> 1) ^ g_swizzle(g_r)) << 5) + ((g_c & 1) << 4);
   const int x_dst = x_r * C::kXRow + ((x_c ^ x_swizzle<BK>(x_r)) << 4);
   const __amdgpu_buffer_rsrc_t s_rsrc = row_rsrc(a.x_scale, a.x_scale_per_row ? (uint32_t)a.m * 4u : 4u);
   const int s_step = a.x_scale_per_row ? 4 : 0;  // bytes from a token's scale to the next one's
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   // lane's base with those bits flipped; rows and sub-steps are constant offsets.
   const int l16 = lane & 15, grp = lane >> 4;
   const int g_row = 8 * grp + (l16 >> 2);
-  const int g_rd = g_row * C::kGRow + (((wn * C::FN) ^ (l16 >> 2)) << 5) + ((l16 & 3) << 3);
+  const int g_rd = g_row * C::kGRow + (((wn * C::FN) ^ g_swizzle(g_row)) << 5) + ((l16 & 3) << 3);
   const int x_row = 8 * grp + (l16 >> 1);
   const int x_rd = x_row * C::kXRow + (((wk * C::FK) ^ x_swizzle<BK>(x_row)) << 4) + ((l16 & 1) << 3);
   uint8_t* const lds_g = lds + ks * 2 * C::kStage;
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
         const wg_s4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5)) + ss * 32 * C::kGRow));
         const wg_s4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5) ^ (4 << 5)) + (ss * 32 + 4) * C::kGRow));
+            (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5)) + (ss * 32 + 4) * C::kGRow));
         f[h][j] = __builtin_bit_cast(wg_b8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
       }
   };
