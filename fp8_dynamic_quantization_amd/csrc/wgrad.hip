@@ -125,12 +125,24 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   float rs[C::kGVec];
   __amdgpu_buffer_rsrc_t g_rsrc, x_rsrc;
   int s_vo;  // byte offset of the scale of the thread's first row; past the extent where the step has no rows
-  auto set_step = [&](int s) {
-    const int64_t m0 = (int64_t)s * MS;
-    const uint32_t rows = s < s_end ? (uint32_t)min((int64_t)MS, a.m - m0) : 0u;
-    g_rsrc = row_rsrc(a.g + (size_t)(rows ? m0 : 0) * a.n + n0, rows ? rows * (uint32_t)a.n * 2u - (uint32_t)n0 * 2u : 0u);
-    x_rsrc = row_rsrc(a.xq + (size_t)(rows ? m0 : 0) * a.k + k0, rows ? rows * (uint32_t)a.k - (uint32_t)k0 : 0u);
-    s_vo = rows ? ((int)m0 + g_r) * s_step : kBadOffset;
+  // The group's next step: first token (past the end it only advances) and the
+  // tokens from there to the part's end.
+  int next_m = (s_begin + ks) * MS;
+  int next_left = min(a.m, s_end * MS) - next_m;
+  const uint32_t n2 = (uint32_t)a.n * 2u, uk = (uint32_t)a.k;
+  const uint8_t* next_g = reinterpret_cast<const uint8_t*>(a.g + (size_t)next_m * a.n + n0);
+  const uint8_t* next_x = a.xq + (size_t)next_m * a.k + k0;
+  const size_t g_adv = (size_t)KS * MS * n2, x_adv = (size_t)KS * MS * uk;
+  auto set_step = [&]() {
+    const bool any = next_left > 0;
+    const uint32_t rows = (uint32_t)min(next_left, MS);
+    g_rsrc = row_rsrc(next_g, any ? rows * n2 - (uint32_t)n0 * 2u : 0u);
+    x_rsrc = row_rsrc(next_x, any ? rows * uk - (uint32_t)k0 : 0u);
+    s_vo = any ? (next_m + g_r) * s_step : kBadOffset;
+    next_g += g_adv;
+    next_x += x_adv;
+    next_m += KS * MS;
+    next_left -= KS * MS;
   };
   auto load_g = [&](int v) {
     rg[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(g_rsrc, g_vo, (int)((uint32_t)(v * C::kGStep) * (uint32_t)a.n * 2u), 0));
@@ -190,40 +202,54 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
         (HQ_LDS wg_i2*)(stage + kXOff + (x_rd ^ ((slot % C::FK) << 4)) + (slot / C::FK) * 32 * C::kXRow));
   };
 
-  // One step of MS tokens as slots of one X fragment each: the next slot's
-  // fragment is read, one staging piece of the next step is converted, stored to
-  // the other stage and replaced by its load for the step after, and the slot's
-  // MFMAs run, so conversions and LDS traffic lie between matrix instructions
-  // instead of before them (2048 x 4096 x 1024: 27.0 us with all staging ahead of
-  // the step's MFMAs). The barriers keep the compiler from gathering them again.
-  constexpr int kSub = MS / 32, kSlots = kSub * C::FK, kPieces = C::kGVec + C::kXVec;
-  static_assert(kPieces <= kSlots, "at most one staging piece per slot");
-  auto step = [&](int buf) {
+  // One step of MS tokens as slots of one X fragment each. A slot reads the X
+  // fragment of two slots ahead, converts the next slot's, runs its own MFMAs and
+  // takes its share of the staging: a piece of the next step is converted, stored
+  // to the other stage and replaced by its load for the step after. The pieces
+  // are all stored two slots before the step ends; the barrier stands there, by
+  // which time every read of this stage has been issued too, and the last two slots
+  // read the next stage's first fragments. So no MFMA waits for LDS at a step's
+  // start, and the VALU work lies between matrix instructions (the group barriers
+  // ask for that order).
+  constexpr int kSub = MS / 32, kSlots = kSub * C::FK, kPieces = C::kGVec + C::kXVec, kFill = kSlots - 2;
+  static_assert(kSlots % 2 == 0 && kFill >= 2, "slots");
+  wg_b8 fg[2][H][C::FN];
+  wg_i2 raw[2];
+  wg_b8 xb[2];
+  auto step = [&](int buf, auto parity) {
+    constexpr int P = kSub > 1 ? 0 : decltype(parity)::value;  // fg of the step's first sub-step
     const uint8_t* cur = lds_g + buf * C::kStage;
     uint8_t* nxt = lds_g + (buf ^ 1) * C::kStage;
-    wg_b8 fg[kSub > 1 ? 2 : 1][H][C::FN];
-    wg_i2 fx[2];
-    read_g(cur, 0, fg[0]);
-    fx[0] = read_x(cur, 0);
 #pragma unroll
     for (int sl = 0; sl < kSlots; ++sl) {
       const int ss = sl / C::FK, i = sl % C::FK;
-      if (sl + 1 < kSlots) fx[(sl + 1) & 1] = read_x(cur, sl + 1);
-      if (i == C::FK / 2 && ss + 1 < kSub) read_g(cur, ss + 1, fg[(ss + 1) & (kSub > 1 ? 1 : 0)]);
-      const wg_b8 x = bf16x8<XF>(fx[sl & 1]);
+      raw[sl & 1] = sl + 2 < kSlots ? read_x(cur, sl + 2) : read_x(nxt, sl + 2 - kSlots);
+      if (i == C::FK / 2 - 1 && ss + 1 < kSub) read_g(cur, ss + 1, fg[(P + ss + 1) & 1]);
+      if (sl == kFill) read_g(nxt, 0, fg[(P + kSub) & 1]);
+      xb[(sl + 1) & 1] = bf16x8<XF>(raw[(sl + 1) & 1]);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, fg[ss & (kSub > 1 ? 1 : 0)][h][j], acc[i][j], 0, 0, 0);
-      if (sl < C::kGVec) {
-        store_g(nxt, sl);
-        load_g(sl);
-      } else if (sl < kPieces) {
-        store_x(nxt, sl - C::kGVec);
-        load_x(sl - C::kGVec);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[sl & 1], fg[(P + ss) & 1][h][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        if (p * kFill / kPieces != sl) continue;
+        if (p < C::kGVec) {
+          store_g(nxt, p);
+          load_g(p);
+        } else {
+          store_x(nxt, p - C::kGVec);
+          load_x(p - C::kGVec);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < H * C::FN; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one matrix instruction,
+        __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // then vector ones
       }
       __builtin_amdgcn_sched_barrier(0);
+      if (sl == kFill - 1) __syncthreads();
     }
   };
 
@@ -231,25 +257,32 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   // both groups of KS == 2 pass the same number of barriers (steps past the end
   // hold zeros).
   const int iters = (max(s_end - s_begin, 0) + KS - 1) / KS;
-  auto load_all = [&](int s) {
-    set_step(s);
+  auto load_all = [&]() {
+    set_step();
 #pragma unroll
     for (int v = 0; v < C::kGVec; ++v) load_g(v);
 #pragma unroll
     for (int v = 0; v < C::kXVec; ++v) load_x(v);
   };
-  load_all(s_begin + ks);
+  load_all();
 #pragma unroll
   for (int v = 0; v < C::kGVec; ++v) store_g(lds_g, v);
 #pragma unroll
   for (int v = 0; v < C::kXVec; ++v) store_x(lds_g, v);
-  load_all(s_begin + ks + KS);
+  load_all();
   __syncthreads();
-  for (int i = 0; i < iters; ++i) {
-    set_step(s_begin + ks + (i + 2) * KS);
-    step(i & 1);
-    __syncthreads();
+  read_g(lds_g, 0, fg[0]);
+  raw[0] = read_x(lds_g, 0);
+  raw[1] = read_x(lds_g, 1);
+  xb[0] = bf16x8<XF>(raw[0]);
+  for (int i = 0; i < iters; i += 2) {
+    set_step();
+    step(0, std::integral_constant<int, 0>{});
+    if (i + 1 == iters) break;
+    set_step();
+    step(1, std::integral_constant<int, 1>{});
   }
+  __syncthreads();
 
   if constexpr (KS == 2) {
     v4f* part = reinterpret_cast<v4f*>(lds);
