@@ -291,17 +291,40 @@ __global__ __launch_bounds__(1024) void act_bwd_columns_kernel(ActBwdArgs a) {
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+// Workgroups beyond this many walk over several rows.
+constexpr int64_t kMaxRowBlocks = 1 << 20;
+
+// Wavefronts per row and vectors per thread; a workgroup per row, or four, as in
+// the norm (8192 x 4096 bf16 SiLU gated with checkpoint: 45.1 us, 5.3 TB/s, with 4 x 2,
+// 49.0 with a grid of 4 workgroups per CU). Two forms serve one width where few
+// rows and many differ (us, 2048 columns not gated: 1000 rows 4.2 with 4 x 1 and 4.7
+// with 1 x 4, 16384 rows 32.8 and 27.6) and where the gated form's registers tell
+// (16384 columns, 2048 rows: gated 50.3 with 8 x 4 and 57.9 with 16 x 2, not gated
+// 30.2 and 27.2).
 template <int XT, int ACT, bool GATED>
 static hipError_t launch_act_a(const ActArgs& a, hipStream_t st) {
   const int nvec = a.cols / VecTraits<XT>::kElems;
-  auto grid = [&](int rows_per) {
-    const int64_t want = ((int64_t)a.rows + rows_per - 1) / rows_per;
-    return dim3((unsigned)(want < kNumCUs * 4 ? want : kNumCUs * 4));
-  };
-  if (nvec <= 64 * 2) hipLaunchKernelGGL((act_quant_kernel<XT, 1, 2, ACT, GATED>), grid(4), dim3(256), 0, st, a);
-  else if (nvec <= 256 * 2) hipLaunchKernelGGL((act_quant_kernel<XT, 4, 2, ACT, GATED>), grid(1), dim3(256), 0, st, a);
-  else if (nvec <= 256 * 8) hipLaunchKernelGGL((act_quant_kernel<XT, 4, 8, ACT, GATED>), grid(1), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((act_quant_long_kernel<XT, ACT, GATED>), grid(1), dim3(1024), 0, st, a);
+#define HQ_LAUNCH(WPR, NV)                                                                                            \
+  do {                                                                                                                \
+    using C = ActFwd<XT, WPR, ACT, GATED>;                                                                            \
+    const int64_t want = ((int64_t)a.rows + C::kRows - 1) / C::kRows;                                                 \
+    hipLaunchKernelGGL((act_quant_kernel<XT, WPR, NV, ACT, GATED>),                                                   \
+                       dim3((unsigned)(want < kMaxRowBlocks ? want : kMaxRowBlocks)), dim3(C::kThreads), 0, st, a);    \
+  } while (0)
+  if (nvec <= 64 * 1) HQ_LAUNCH(1, 1);
+  else if (nvec <= 64 * 2) HQ_LAUNCH(1, 2);
+  else if (nvec <= 64 * 4 && a.rows < 4096) HQ_LAUNCH(4, 1);
+  else if (nvec <= 64 * 4) HQ_LAUNCH(1, 4);
+  else if (nvec <= 256 * 2) HQ_LAUNCH(4, 2);
+  else if (nvec <= 512 * 2) HQ_LAUNCH(8, 2);
+  else if (nvec <= 512 * 4) {
+    if constexpr (GATED || XT == kF32) HQ_LAUNCH(8, 4);
+    else HQ_LAUNCH(16, 2);
+  } else if (nvec <= 1024 * 4) HQ_LAUNCH(16, 4);
+  else
+    hipLaunchKernelGGL((act_quant_long_kernel<XT, ACT, GATED>),
+                       dim3((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), dim3(1024), 0, st, a);
+#undef HQ_LAUNCH
   return hipGetLastError();
 }
 

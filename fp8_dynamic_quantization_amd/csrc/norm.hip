@@ -507,25 +507,40 @@ hipError_t launch_column_sums(const float* partials, int parts, int cols, float*
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+// Workgroups beyond this many walk over several rows (a launch holds fewer than
+// 2^32 threads).
+constexpr int64_t kMaxRowBlocks = 1 << 20;
+
 template <int XT, int WPR, int NV>
 static hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
   using C = NormFwd<XT, WPR, NV>;
   const int64_t want = ((int64_t)a.rows + C::kRows - 1) / C::kRows;
-  const int grid = (int)(want < kNumCUs * 4 ? want : kNumCUs * 4);
-  hipLaunchKernelGGL((rmsnorm_quant_kernel<XT, WPR, NV>), dim3(grid), dim3(C::kThreads), 0, st, a);
+  hipLaunchKernelGGL((rmsnorm_quant_kernel<XT, WPR, NV>), dim3((unsigned)(want < kMaxRowBlocks ? want : kMaxRowBlocks)),
+                     dim3(C::kThreads), 0, st, a);
   return hipGetLastError();
 }
 
+// Wavefronts per row and vectors per thread. A workgroup per row (or four) leaves
+// the overlap of one row's latency with another's traffic to the scheduler:
+// 16384 x 4096 bf16 with residual and checkpoint takes 93.6 us (5.8 TB/s) with
+// 4 x 2 that way, 106 us with a grid of 4 workgroups per CU that walk over the
+// rows, and 113 us with one wavefront per row and 8 vectors, whose registers hold
+// two wavefronts per SIMD. Where two forms serve one width the first is for few
+// rows, whose latency counts (us, 7168 columns: one row 3.9 with 8 x 2 and 4.7
+// with 4 x 4, 4681 rows 53.2 and 51.1; 2048 columns: 1000 rows 4.8 with 4 x 1 and
+// 5.4 with 1 x 4, 16384 rows 53.0 and 49.3).
 template <int XT>
 static hipError_t launch_norm_x(const NormArgs& a, hipStream_t st) {
   const int nvec = a.cols / VecTraits<XT>::kElems;
+  if (nvec <= 64 * 1) return launch_norm_t<XT, 1, 1>(a, st);
   if (nvec <= 64 * 2) return launch_norm_t<XT, 1, 2>(a, st);
-  if (nvec <= 64 * 8) return launch_norm_t<XT, 1, 8>(a, st);
-  if (nvec <= 256 * 4) return launch_norm_t<XT, 4, 4>(a, st);
-  if (nvec <= 256 * 8) return launch_norm_t<XT, 4, 8>(a, st);
+  if (nvec <= 64 * 4) return a.rows < 4096 ? launch_norm_t<XT, 4, 1>(a, st) : launch_norm_t<XT, 1, 4>(a, st);
+  if (nvec <= 256 * 2) return launch_norm_t<XT, 4, 2>(a, st);
+  if (nvec <= 256 * 4) return a.rows < 1024 ? launch_norm_t<XT, 8, 2>(a, st) : launch_norm_t<XT, 4, 4>(a, st);
+  if (nvec <= 512 * 4) return launch_norm_t<XT, 8, 4>(a, st);
   if (nvec <= 1024 * 4) return launch_norm_t<XT, 16, 4>(a, st);
-  const int grid = a.rows < kNumCUs * 2 ? a.rows : kNumCUs * 2;
-  hipLaunchKernelGGL((rmsnorm_quant_long_kernel<XT>), dim3(grid), dim3(1024), 0, st, a);
+  hipLaunchKernelGGL((rmsnorm_quant_long_kernel<XT>), dim3((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)),
+                     dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

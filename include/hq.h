@@ -611,7 +611,7 @@ hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, i
  * Requires cols % 16 == 0 and, gated with a checkpoint, cols % block_size == 0
  * (no block spans both halves); rows, 2 * cols <= 2^31 - 1024, rows * cols < 2^40;
  * no output may overlap another buffer. rows == 0 returns HQ_OK without a launch.
- * Rows of up to 16384 bf16 (8192 float32) elements of `a` are read once, longer
+ * Rows of up to 32768 bf16 (16384 float32) elements of `a` are read once, longer
  * ones twice. */
 hq_status hq_act_quantize_fp8(const void* z, int xt, int64_t rows, int64_t cols, int act, int gated, int fmt, uint8_t* q,
                               float* scale_out, const hq_checkpoint* ckpt, hipStream_t stream);
