@@ -216,9 +216,9 @@ __global__ __launch_bounds__(1024) void act_bwd_kernel(ActBwdArgs a) {
     float o1[E], o2[E];
     act_bwd_vec<XT, ACT, GATED>(dav, w1, sz1, w2, sz2, o1, o2, db);
     uint8_t* out = static_cast<uint8_t*>(a.dz) + ((size_t)row * wide + c0) * (16 / E);
-    row_store16<kStreamPolicy>(row_rsrc(out, left * (16 / E)), t * 16, vec_narrow<XT>(o1));
+    row_store16<0>(row_rsrc(out, left * (16 / E)), t * 16, vec_narrow<XT>(o1));
     if constexpr (GATED)
-      row_store16<kStreamPolicy>(row_rsrc(out + (size_t)a.cols * (16 / E), left * (16 / E)), t * 16, vec_narrow<XT>(o2));
+      row_store16<0>(row_rsrc(out + (size_t)a.cols * (16 / E), left * (16 / E)), t * 16, vec_narrow<XT>(o2));
   }
   if (!a.partials) return;
 
@@ -366,7 +366,7 @@ static ActBwdPlan act_bwd_plan(int rows, int cols, int xt) {
   p.tiles = (nvec + 64 * p.cw - 1) / (64 * p.cw);
   const int groups = 16 / p.cw;
   const int64_t want = ((int64_t)rows + groups - 1) / groups;
-  const int64_t fill = (2 * kNumCUs + p.tiles - 1) / p.tiles;  // two workgroups per CU
+  const int64_t fill = (kNumCUs + p.tiles - 1) / p.tiles;  // one workgroup per CU
   p.parts = (int)(want < fill ? want : fill);
   p.direct = rows <= kDirectRows && (int64_t)rows * cols * (xt == kBF16 ? 2 : 4) <= kDirectBytes;
   return p;

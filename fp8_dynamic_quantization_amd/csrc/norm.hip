@@ -359,7 +359,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int ro
         const float n = fmaf(-xh[j][e], c, tt) * rstd;
         o[e] = a.dres ? n + vec_elem<XT>(rv[j], e) : n;
       }
-      row_store16<kStreamPolicy>(o_rsrc, off0 + j * 16 * kRowThreads, vec_narrow<XT>(o));
+      row_store16<0>(o_rsrc, off0 + j * 16 * kRowThreads, vec_narrow<XT>(o));
     }
   }
   if (!a.partials) return;
