@@ -243,6 +243,19 @@ def test_act_quantize(hq, rows, cols, xt, act, gated, block, fmt):
         assert c is None
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_act_quantize_longest_rows(hq, gated):
+    """Rows past the register form in bf16."""
+    test_act_quantize(hq, 3, 32896, Q.BF16, "silu", gated, 128, fp8.E4M3)
+
+
+@pytest.mark.parametrize("m", [17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("n,k", [(40, 2064), (4104, 144), (8, 16)])
+def test_gemm_fused_row_blocks(hq, m, n, k):
+    """Each count of 16-row blocks, one weight fragment per workgroup and two, K tails."""
+    test_gemm_fused(hq, m, n, k, "silu", True, True, False)
+
+
 @pytest.mark.parametrize("cols", [1040, 20496])
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
 def test_act_quantize_ragged_blocks_and_nonfinite(hq, cols, act):
