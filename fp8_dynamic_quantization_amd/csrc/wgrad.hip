@@ -13,12 +13,20 @@
 // so one 8-bit and two 16-bit reads give the operands of V_MFMA_F32_16X16X32_BF16,
 // whose lane l holds contraction values 8 (l / 16) .. +7 of row or column l % 16.
 //
-// The FP8 codes are exact in bf16 and are converted after the read. The token's
-// scale is folded into G on its way to LDS, once per workgroup: rounded to bf16
-// (2^-8 of a term at most), or as the sum of two bf16 numbers (hi = bf16(v), lo =
-// bf16(v - hi): 2^-17 of a term is left over) whose products are both added, for
-// a float32 result and wherever few tokens leave little to average the terms'
-// roundings over.
+// The FP8 codes are exact in bf16 and in f16 and are converted after the read. The
+// token's scale is folded into G on its way to LDS, once per workgroup. Two forms:
+//   one number   v = g * scale rounded to bf16, at most 2^-8 of a term: for a bf16
+//                result, whose own rounding is as large as what is left of the terms'
+//                after they are summed
+//   two numbers  v = hi + lo in f16, both multiplied (V_MFMA_F32_16X16X32_F16, the
+//                same rate): 2^-23 of a term. f16's range is covered by scaling each
+//                column of G by the power of two that takes the largest |g * scale|
+//                of the column below 2^15, undone on the sums (both exact); a term
+//                2^29 below its column's largest starts to lose bits, by 2^-40 of
+//                that largest. (Two bf16 numbers need no scaling but leave 2^-17 of a
+//                term: 1.1e-6 of a result, against 6e-8 for float32 arithmetic.)
+//                For a float32 result, and for few tokens, which leave little to
+//                average the terms' roundings over.
 #include "gemm_kernels.h"
 #include "hq_row.h"
 
@@ -27,6 +35,7 @@ namespace hq {
 typedef short wg_s4 __attribute__((ext_vector_type(4)));
 typedef int wg_i2 __attribute__((ext_vector_type(2)));
 typedef __bf16 wg_b8 __attribute__((ext_vector_type(8)));
+typedef int wg_i4 __attribute__((ext_vector_type(4)));
 #define HQ_LDS __attribute__((address_space(3)))
 
 // BN x BK outputs per workgroup of 8 wavefronts. KS = 1: 4 wavefronts along n, 2
@@ -61,8 +70,10 @@ __device__ __forceinline__ int x_swizzle(int row) {
   return BK == 256 ? row & 15 : (row >> 1) & 7;
 }
 
-template <int XF>
-__device__ __forceinline__ wg_b8 bf16x8(wg_i2 c) {
+// Eight codes as operand values of the form, and its matrix instruction.
+template <int XF, bool HILO>
+__device__ __forceinline__ wg_i4 decode8(wg_i2 c) {
+  if constexpr (HILO) return __builtin_bit_cast(wg_i4, f16x8<XF>((uint32_t)c[0], (uint32_t)c[1]));
   bf2v v[4];
   if constexpr (XF == kE4M3) {
     v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, false);
@@ -75,7 +86,50 @@ __device__ __forceinline__ wg_b8 bf16x8(wg_i2 c) {
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[1], 1.0f, false);
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[1], 1.0f, true);
   }
-  return wg_b8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+  return __builtin_bit_cast(wg_i4, wg_b8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]});
+}
+template <bool HILO>
+__device__ __forceinline__ v4f wg_mfma(wg_i4 x, wg_i4 g, v4f acc) {
+  if constexpr (HILO)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, x), __builtin_bit_cast(h8v, g), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(wg_b8, x), __builtin_bit_cast(wg_b8, g), acc, 0, 0, 0);
+}
+
+// Largest finite |g * scale| of the 8 columns of a vector, as float32 bits, into m.
+__device__ __forceinline__ void max8(const uint4& g, float scale, uint32_t* m) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(vec_elem<kBF16>(g, e) * scale) & 0x7fffffffu;
+    m[e] = max(m[e], b < kInfBits ? b : 0u);
+  }
+}
+// The power of two that takes values up to m below 2^15.
+__device__ __forceinline__ int f16_exponent(uint32_t m) { return m ? 141 - (int)(m >> 23) : 0; }
+
+// Largest finite |g * scale| per column over one of gridDim.y runs of tokens: 512
+// columns per workgroup, a wavefront per token.
+__global__ __launch_bounds__(1024) void wgrad_colmax_kernel(WgradArgs a, int rows_per_part, uint32_t* out) {
+  __shared__ uint32_t s[16][64][8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (blockIdx.x * 64 + lane) * 8;
+  const int m1 = min(a.m, (int)(blockIdx.y + 1) * rows_per_part);
+  uint32_t m[8] = {};
+  if (c < a.n) {
+#pragma unroll 8
+    for (int r = blockIdx.y * rows_per_part + wave; r < m1; r += 16)
+      max8(*reinterpret_cast<const uint4*>(a.g + (size_t)r * a.n + c), a.x_scale[a.x_scale_per_row ? r : 0], m);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[wave][lane][e] = m[e];
+  __syncthreads();
+  if (threadIdx.x >= 512) return;
+  const int l = threadIdx.x >> 3, e = threadIdx.x & 7;
+  uint32_t v = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) v = max(v, s[w][l][e]);
+  const int col = (blockIdx.x * 64 + l) * 8 + e;
+  if (col < a.n) out[(size_t)blockIdx.y * a.n + col] = v;
 }
 
 // Steps [step0, step1) of MS tokens; `part` selects the partial-sum slab when the
@@ -107,6 +161,40 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   const __amdgpu_buffer_rsrc_t s_rsrc = row_rsrc(a.x_scale, a.x_scale_per_row ? (uint32_t)a.m * 4u : 4u);
   const int s_step = a.x_scale_per_row ? 4 : 0;  // bytes from a token's scale to the next one's
   constexpr int H = HILO ? 2 : 1;
+
+  // Two numbers: the exponents of the tile's columns, from the maxima that a pass
+  // before this one wrote, or from the tile's own columns.
+  __shared__ __attribute__((aligned(16))) int s_exp[HILO ? BN : 4];
+  if constexpr (HILO) {
+    uint32_t* s_max = reinterpret_cast<uint32_t*>(lds);
+    constexpr int kRowsAt = C::kThreads / (BN / 8);
+    static_assert(kRowsAt * BN * 4 <= C::kLds, "the columns' maxima fit the stages");
+    if (!a.colmax) {
+      const int c = threadIdx.x % (BN / 8), r0 = threadIdx.x / (BN / 8);
+      uint32_t m[8] = {};
+      if (n0 + c * 8 < a.n) {
+        const int m1 = min(a.m, s_end * MS);
+#pragma unroll 16
+        for (int r = s_begin * MS + r0; r < m1; r += kRowsAt)
+          max8(*reinterpret_cast<const uint4*>(a.g + (size_t)r * a.n + n0 + c * 8), a.x_scale[a.x_scale_per_row ? r : 0], m);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_max[r0 * BN + c * 8 + e] = m[e];
+      __syncthreads();
+    }
+    if (threadIdx.x < BN) {
+      uint32_t m = 0;
+      if (!a.colmax) {
+#pragma unroll
+        for (int r = 0; r < kRowsAt; ++r) m = max(m, s_max[r * BN + threadIdx.x]);
+      } else if (n0 + (int)threadIdx.x < a.n) {
+#pragma unroll 8
+        for (int r = 0; r < a.colmax_parts; ++r) m = max(m, a.colmax[(size_t)r * a.n + n0 + threadIdx.x]);
+      }
+      s_exp[threadIdx.x] = f16_exponent(m);
+    }
+    __syncthreads();
+  }
 
   // Operand reads. The swizzle only touches address bits below the row, and a
   // fragment's number only bits of the unit, so a fragment's address is the
@@ -155,25 +243,27 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
-      hi[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2v));
+      f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
       if constexpr (HILO) {
-        const f2v q = {p[0] - bf16_lo(hi[e]), p[1] - bf16_hi(hi[e])};
-        lo[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(q, bf2v));
+        const int* ex = s_exp + g_c * 8 + 2 * e;  // read at each use: registers are short
+        p = f2v{__builtin_ldexpf(p[0], ex[0]), __builtin_ldexpf(p[1], ex[1])};
+        const h2v h = __builtin_convertvector(p, h2v);
+        hi[e] = __builtin_bit_cast(uint32_t, h);
+        // v - hi in one instruction with hi as f16 (exact). It is at most 8; the clamp turns the NaN that an infinite or NaN hi
+        // leaves into a finite lo, which adds nothing to it
+        f2v q;
+        asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(q[0]) : "v"(hi[e]), "v"(p[0]));
+        asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(q[1]) : "v"(hi[e]), "v"(p[1]));
+        q = f2v{__builtin_amdgcn_fmed3f(q[0], -8.0f, 8.0f), __builtin_amdgcn_fmed3f(q[1], -8.0f, 8.0f)};
+        const h2v l = __builtin_convertvector(q, h2v);
+        lo[e] = __builtin_bit_cast(uint32_t, l);
+      } else {
+        hi[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2v));
       }
     }
-    const uint4 hv = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(stage + g_dst + v * C::kGStep * C::kGRow) = hv;
-    if constexpr (HILO) {
-      if (__any(vec_absmax_raw<kBF16>(hv) >= kInfBits)) {  // rare: an infinite or NaN hi carries the value alone
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((hi[e] & 0x7f80u) == 0x7f80u) lo[e] &= 0xffff0000u;
-          if ((hi[e] & 0x7f800000u) == 0x7f800000u) lo[e] &= 0xffffu;
-        }
-      }
+    *reinterpret_cast<uint4*>(stage + g_dst + v * C::kGStep * C::kGRow) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (HILO)
       *reinterpret_cast<uint4*>(stage + C::kGBytes + g_dst + v * C::kGStep * C::kGRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
   };
   auto store_x = [&](uint8_t* stage, int v) {
     *reinterpret_cast<uint4*>(stage + kXOff + x_dst + v * C::kXStep * C::kXRow) = rx[v];
@@ -185,7 +275,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto read_g = [&](const uint8_t* stage, int ss, wg_b8 (&f)[H][C::FN]) {
+  auto read_g = [&](const uint8_t* stage, int ss, wg_i4 (&f)[H][C::FN]) {
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -194,7 +284,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
             (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5)) + ss * 32 * C::kGRow));
         const wg_s4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (HQ_LDS wg_s4*)(stage + h * C::kGBytes + (g_rd ^ (j << 5)) + (ss * 32 + 4) * C::kGRow));
-        f[h][j] = __builtin_bit_cast(wg_b8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+        f[h][j] = __builtin_bit_cast(wg_i4, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
       }
   };
   auto read_x = [&](const uint8_t* stage, int slot) -> wg_i2 {
@@ -213,25 +303,24 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   // ask for that order).
   constexpr int kSub = MS / 32, kSlots = kSub * C::FK, kPieces = C::kGVec + C::kXVec, kFill = kSlots - 2;
   static_assert(kSlots % 2 == 0 && kFill >= 2, "slots");
-  wg_b8 fg[2][H][C::FN];
+  wg_i4 fg[2][H][C::FN];
   wg_i2 raw[2];
-  wg_b8 xb[2];
-  auto step = [&](int buf, auto parity) {
-    constexpr int P = kSub > 1 ? 0 : decltype(parity)::value;  // fg of the step's first sub-step
+  wg_i4 xb[2];
+  auto step = [&](int buf) {
     const uint8_t* cur = lds_g + buf * C::kStage;
     uint8_t* nxt = lds_g + (buf ^ 1) * C::kStage;
 #pragma unroll
     for (int sl = 0; sl < kSlots; ++sl) {
       const int ss = sl / C::FK, i = sl % C::FK;
       raw[sl & 1] = sl + 2 < kSlots ? read_x(cur, sl + 2) : read_x(nxt, sl + 2 - kSlots);
-      if (i == C::FK / 2 - 1 && ss + 1 < kSub) read_g(cur, ss + 1, fg[(P + ss + 1) & 1]);
-      if (sl == kFill) read_g(nxt, 0, fg[(P + kSub) & 1]);
-      xb[(sl + 1) & 1] = bf16x8<XF>(raw[(sl + 1) & 1]);
+      if (i == C::FK / 2 - 1 && ss + 1 < kSub) read_g(cur, ss + 1, fg[(ss + 1) & 1]);
+      if (kSub % 2 == 0 && sl == kFill) read_g(nxt, 0, fg[0]);
+      xb[(sl + 1) & 1] = decode8<XF, HILO>(raw[(sl + 1) & 1]);
 #pragma unroll
       for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[sl & 1], fg[(P + ss) & 1][h][j], acc[i][j], 0, 0, 0);
+          acc[i][j] = wg_mfma<HILO>(xb[sl & 1], fg[ss & 1][h][j], acc[i][j]);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         if (p * kFill / kPieces != sl) continue;
@@ -249,6 +338,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
         __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // then vector ones
       }
       __builtin_amdgcn_sched_barrier(0);
+      if (kSub % 2 == 1 && sl == kSlots - 1) read_g(nxt, 0, fg[0]);
       if (sl == kFill - 1) __syncthreads();
     }
   };
@@ -274,13 +364,23 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   read_g(lds_g, 0, fg[0]);
   raw[0] = read_x(lds_g, 0);
   raw[1] = read_x(lds_g, 1);
-  xb[0] = bf16x8<XF>(raw[0]);
-  for (int i = 0; i < iters; i += 2) {
-    set_step();
-    step(0, std::integral_constant<int, 0>{});
-    if (i + 1 == iters) break;
-    set_step();
-    step(1, std::integral_constant<int, 1>{});
+  xb[0] = decode8<XF, HILO>(raw[0]);
+  if constexpr (kSub % 2 == 0) {
+    // two steps per iteration: the stages' offsets are constants
+    for (int i = 0; i < iters; i += 2) {
+      set_step();
+      step(0);
+      if (i + 1 == iters) break;
+      set_step();
+      step(1);
+    }
+  } else {
+    // one; its fragments of G are read after the step before's last MFMAs (reading them
+    // earlier into registers of their own took 256 registers and spilled)
+    for (int i = 0; i < iters; ++i) {
+      set_step();
+      step(i & 1);
+    }
   }
   __syncthreads();
 
@@ -306,12 +406,17 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   for (int j = 0; j < C::FN; ++j) {
     const int n = n0 + wn * C::WN + j * 16 + l16;
     if (n >= a.n) continue;
+    const int back = HILO ? -s_exp[wn * C::WN + j * 16 + l16] : 0;
 #pragma unroll
     for (int i = 0; i < C::FK; ++i) {
       const int k = k0 + wk * C::WK + i * 16 + 4 * grp;
       if (k >= a.k) continue;
       const size_t at = (size_t)n * a.k + k;
       v4f v = acc[i][j];
+      if constexpr (HILO) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], back);
+      }
       if (partials) {
         *reinterpret_cast<v4f*>(partials + (size_t)blockIdx.y * a.n * a.k + at) = v;
         continue;
@@ -344,19 +449,25 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict_
   }
 }
 
-// Up to this many tokens a bf16 result, too, carries g * scale in two numbers: the
-// call's time is that of writing dW.
+// Up to this many tokens a bf16 result, too, takes the two-number form: the call's
+// time is that of writing dW.
 constexpr int kWgTwoNumbersM = 64;
+// Up to this many tokens a workgroup of that form finds its columns' maxima itself,
+// a few reads; beyond, a pass of its own reads G once for all.
+constexpr int kWgOwnMaxM = 512;
 
 // Launch plan: the 256 x 256 tile where its tiles fill the CUs, else 128 x 128;
 // where those leave CUs idle too and there are many tokens, the tokens are split.
+// Workspace: the columns' maxima [max_parts, n], then the partial sums [parts, n, k].
 struct WgPlan {
-  bool big;
-  int tiles_n, tiles_k, steps, parts;
+  bool hilo, big;
+  int tiles_n, tiles_k, steps, parts, max_parts;
+  size_t max_bytes, bytes;
 };
-static WgPlan wgrad_plan(int m, int n, int k, bool hilo) {
-  const int ms = hilo ? 32 : 64;
-  WgPlan p;
+static WgPlan wgrad_plan(int m, int n, int k, bool out_f32) {
+  WgPlan p{};
+  p.hilo = out_f32 || m <= kWgTwoNumbersM;
+  const int ms = p.hilo ? 32 : 64;
   auto tiles = [&](int b) { return (int64_t)((n + b - 1) / b) * ((k + b - 1) / b); };
   p.big = tiles(256) >= kNumCUs * 3 / 4;
   const int b = p.big ? 256 : 128;
@@ -366,25 +477,36 @@ static WgPlan wgrad_plan(int m, int n, int k, bool hilo) {
   p.parts = 1;
   while (!p.big && tiles(b) * p.parts * 2 <= kNumCUs && nsteps >= p.parts * 2 * 8) p.parts *= 2;
   p.steps = (nsteps + p.parts - 1) / p.parts;
+  if (p.hilo && m > kWgOwnMaxM) {
+    const int xb = (n + 511) / 512;
+    p.max_parts = xb >= kNumCUs ? 1 : kNumCUs / xb < 32 ? kNumCUs / xb : 32;
+  }
+  p.max_bytes = (size_t)p.max_parts * n * 4;
+  p.bytes = p.max_bytes + (p.parts > 1 ? (size_t)p.parts * n * k * 4 : 0);
   return p;
 }
 
-static bool wgrad_hilo(int m, bool out_f32) { return out_f32 || m <= kWgTwoNumbersM; }
-
-size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32) {
-  const WgPlan p = wgrad_plan(m, n, k, wgrad_hilo(m, out_f32));
-  return p.parts == 1 ? 0 : (size_t)p.parts * n * k * 4;
-}
+size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32) { return wgrad_plan(m, n, k, out_f32).bytes; }
 
 template <int XF, bool HILO>
-static hipError_t launch_wgrad_t(const WgradArgs& a, void* workspace, size_t workspace_bytes, hipStream_t st) {
+static hipError_t launch_wgrad_t(WgradArgs a, WgPlan p, uint8_t* workspace, size_t workspace_bytes, hipStream_t st) {
   constexpr int MS = HILO ? 32 : 64;
-  WgPlan p = wgrad_plan(a.m, a.n, a.k, HILO);
-  if (p.parts > 1 && workspace_bytes < (size_t)p.parts * a.n * a.k * 4) {
+  float* partials = nullptr;
+  if (p.parts > 1 && workspace_bytes >= p.bytes) {
+    partials = reinterpret_cast<float*>(workspace + p.max_bytes);
+  } else {
     p.steps *= p.parts;
     p.parts = 1;
   }
-  float* partials = p.parts > 1 ? static_cast<float*>(workspace) : nullptr;
+  if (p.max_parts > 0 && workspace_bytes >= p.max_bytes) {
+    uint32_t* out = reinterpret_cast<uint32_t*>(workspace);
+    hipLaunchKernelGGL(wgrad_colmax_kernel, dim3((a.n + 511) / 512, p.max_parts), dim3(1024), 0, st, a,
+                       (a.m + p.max_parts - 1) / p.max_parts, out);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.colmax = out;
+    a.colmax_parts = p.max_parts;
+  }
   const dim3 grid(p.tiles_n * p.tiles_k, p.parts);
   if (p.big)
     hipLaunchKernelGGL((wgrad_kernel<XF, 256, 256, 1, MS, HILO>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
@@ -401,11 +523,12 @@ static hipError_t launch_wgrad_t(const WgradArgs& a, void* workspace, size_t wor
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st) {
-  const bool hilo = wgrad_hilo(a.m, a.out_f32);
-  if (xf == kE4M3) return hilo ? launch_wgrad_t<kE4M3, true>(a, workspace, workspace_bytes, st)
-                               : launch_wgrad_t<kE4M3, false>(a, workspace, workspace_bytes, st);
-  return hilo ? launch_wgrad_t<kE5M2, true>(a, workspace, workspace_bytes, st)
-              : launch_wgrad_t<kE5M2, false>(a, workspace, workspace_bytes, st);
+  const WgPlan p = wgrad_plan(a.m, a.n, a.k, a.out_f32);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (xf == kE4M3) return p.hilo ? launch_wgrad_t<kE4M3, true>(a, p, ws, workspace_bytes, st)
+                                 : launch_wgrad_t<kE4M3, false>(a, p, ws, workspace_bytes, st);
+  return p.hilo ? launch_wgrad_t<kE5M2, true>(a, p, ws, workspace_bytes, st)
+                : launch_wgrad_t<kE5M2, false>(a, p, ws, workspace_bytes, st);
 }
 
 }  // namespace hq

@@ -652,13 +652,15 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
  *   dw         device, [n, k] of dwt (HQ_BF16 or HQ_F32)
  *   workspace  device, workspace_bytes bytes, 16-byte aligned, or NULL with 0.
  *              Needs no initial value. With hq_wgrad_workspace_bytes(m, n, k, dwt)
- *              bytes a gradient of few tiles is split over the tokens; with less it
- *              is not, slower, and its sums are associated otherwise. Calls that
+ *              bytes a gradient of few tiles is split over the tokens, and the
+ *              columns' largest terms are found once for all tiles; with less the
+ *              call is slower, and its sums may be associated otherwise. Calls that
  *              share one must not run concurrently
- * Products run on the bf16 matrix cores with float32 sums. For a bf16 result of
+ * Products run on the 16-bit matrix cores with float32 sums. For a bf16 result of
  * more than 64 tokens g * x_scale[m] is rounded to bf16 (at most 2^-8 of a term,
- * beside the result's own rounding); otherwise it is carried as two bf16 numbers,
- * exact to 2^-17 of a term, at twice the matrix-core work.
+ * beside the result's own rounding). Otherwise it is carried as two f16 numbers,
+ * exact to 2^-23 of a term or 2^-40 of the largest |g * x_scale| of its column n,
+ * whichever is more, at twice the matrix-core work.
  * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n, m * k and n * k < 2^40; 16-byte aligned g, xq, base, dw; no output may overlap an input
  * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
  * base, or zeros. */

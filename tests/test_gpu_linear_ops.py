@@ -437,6 +437,45 @@ def test_wgrad_nonfinite_stay_in_their_row_and_column(hq):
     assert int((~keep).sum()) == 272 + 264 - 1 and torch.equal(dw[keep], clean.float()[keep])
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 64, 48), (500, 136, 144), (700, 264, 272), (3000, 72, 80)])
+@pytest.mark.parametrize("xf", [fp8.E4M3, fp8.E5M2])
+def test_wgrad_two_numbers_over_a_wide_range(hq, m, n, k, xf):
+    """A float32 gradient whose columns span 2^-100 .. 2^60 and whose terms within a
+    column span 2^20: each term is exact to 2^-23 of itself or 2^-40 of the column's
+    largest |g * scale|; m additions follow."""
+    rng = np.random.default_rng(77)
+    col = 2.0 ** rng.integers(-100, 61, n)
+    row = 2.0 ** -rng.integers(0, 21, m)
+    gv = (rng.standard_normal((m, n)) * col * row[:, None]).astype(np.float32)
+    gv[:, 3] = 0.0
+    bits = workloads.to_bf16_bits(gv)
+    gv = workloads.bf16_bits_to_f32(bits)
+    xq = narrow_codes(rng, (m, k), xf)
+    xs = rng.uniform(0.5, 2.0, m).astype(np.float32)
+    ref, a = L.wgrad(gv, xq, xf, xs)
+    top = np.abs(gv * xs[:, None].astype(np.float64)).max(axis=0)
+    tol = a * (2.0 ** -23 + (m + 64) * U) + top[:, None] * 2.0 ** -40 * np.abs(fp8.decode(xq, xf)).sum(axis=0) + 2.0 ** -126
+    for ws in (None, False):
+        dw = hq.hq_wgrad_a8(dev_bf16(bits), dev_u8(xq), xf, dev_f32(xs), dtype=torch.float32, workspace=ws)
+        err = np.abs(_f64(dw) - ref)
+        assert np.all(err <= tol + U * np.abs(ref)), f"{np.max(err / (tol + U * np.abs(ref)))} of the bound"
+
+
+def test_wgrad_infinite_gradient_in_two_numbers(hq):
+    rng = np.random.default_rng(78)
+    g, _ = _make(rng, (40, 64), Q.BF16)
+    xq = narrow_codes(rng, (40, 48), fp8.E4M3, zero_frac=0.0)
+    xs = dev_f32(rng.uniform(0.5, 1.0, 40))
+    clean = host(hq.hq_wgrad_a8(g, dev_u8(xq), fp8.E4M3, xs, dtype=torch.float32))
+    g[7, 5] = float("inf")
+    g[9, 6] = float("nan")
+    dw = host(hq.hq_wgrad_a8(g, dev_u8(xq), fp8.E4M3, xs, dtype=torch.float32))
+    assert np.array_equal(dw[5], np.where(xq[7] & 0x80, -np.inf, np.inf))
+    assert np.isnan(dw[6]).all()
+    keep = np.delete(np.arange(64), [5, 6])
+    assert np.array_equal(dw[keep], clean[keep])
+
+
 def test_empty_batches(hq):
     e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
     out = hq.hq_rmsnorm_quantize_fp8(e(0, 64), e(64), EPS, residual=e(0, 64), checkpoint=32)
