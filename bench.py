@@ -48,8 +48,8 @@ NUM_CUS = 256
 QUANT_ROW_WAVES_PER_CU = 12         # the per-token quantize's grid (wavefronts per compute unit)
 ROW_PROBE_WAVES_PER_CU = (4, 8, 12, 16)
 COPY_PROBE_KERNEL = "bitwise_not"
-KERNEL_SOURCES = ["fp8_dynamic_quantization_amd/csrc/gemm.hip", "fp8_dynamic_quantization_amd/csrc/quantize.hip",
-                  "fp8_dynamic_quantization_amd/csrc/hq_device.h"]
+KERNEL_SOURCES = ["fp8_dynamic_quantization_amd/csrc/gemm.hip", "fp8_dynamic_quantization_amd/csrc/gemm_kernels.h",
+                  "fp8_dynamic_quantization_amd/csrc/quantize.hip", "fp8_dynamic_quantization_amd/csrc/hq_device.h"]
 
 
 def log(*a):
