@@ -178,7 +178,10 @@ __device__ __forceinline__ void act_bwd_vec(const uint4& dav, const uint32_t* w1
 // 64 CW vectors of columns and walks down the rows, 16 / CW rows at a time; a
 // thread keeps its columns' sums of dz in registers (unrounded), the row groups
 // meet in LDS at the end, and one partial row per workgroup goes to the
-// workspace for column_sums_kernel.
+// workspace for column_sums_kernel. dz goes through the caches: 8192 x 4096 bf16 SiLU
+// gated (271 MB, 52.6 us at a large copy's 5.15 TB/s) takes 49.1 us replayed from a
+// graph, 55.5 with dz streamed past them and two workgroups per CU; 52.6 with runs of
+// neighbouring rows per workgroup.
 template <int XT, int CW, int ACT, bool GATED>
 __global__ __launch_bounds__(1024) void act_bwd_kernel(ActBwdArgs a) {
   constexpr int E = VecTraits<XT>::kElems;

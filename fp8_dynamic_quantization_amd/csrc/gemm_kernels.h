@@ -37,7 +37,6 @@
 #include "hq_device.h"
 #include "hq_launch.h"
 
-#include <type_traits>
 
 namespace hq {
 

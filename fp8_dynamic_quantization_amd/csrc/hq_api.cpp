@@ -1015,7 +1015,7 @@ hq_status hq_act_backward(const void* da, const hq_checkpoint* ckpt, int xt, int
 
 static bool wgrad_sizes(int64_t m, int64_t n, int64_t k) {
   return m >= 0 && n >= 0 && k >= 0 && m < (1 << 28) && n < (1 << 24) && k < (1 << 24) && n % 8 == 0 && k % 16 == 0 &&
-         (double)m * n < 1099511627776.0 && (double)m * k < 1099511627776.0 && (double)n * k < 1099511627776.0;
+         (double)m * n < 1099511627776.0 && (double)m * k < 1099511627776.0 && (double)n * k < 274877906944.0;
 }
 
 int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt) {
@@ -1031,7 +1031,7 @@ hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float*
   if (dwt != HQ_BF16 && dwt != HQ_F32) return fail(HQ_ERR_INVALID_ARGUMENT, "dwt must be HQ_F32 or HQ_BF16, got %d", dwt);
   if (!wgrad_sizes(m, n, k))
     return fail(HQ_ERR_INVALID_ARGUMENT, "m must be in [0, 2^28), n and k in [0, 2^24) with n %% 8 == 0, k %% 16 == 0 and "
-                "every tensor below 2^40 elements, got %lld, %lld, %lld", (long long)m, (long long)n, (long long)k);
+                "g and xq below 2^40, dw below 2^38 elements, got %lld, %lld, %lld", (long long)m, (long long)n, (long long)k);
   if (x_scale_count != 1 && x_scale_count != m)
     return fail(HQ_ERR_INVALID_ARGUMENT, "x_scale_count must be 1 or m (%lld), got %lld", (long long)m, (long long)x_scale_count);
   if (base && dwt != HQ_F32) return fail(HQ_ERR_INVALID_ARGUMENT, "base needs a float32 dw");

@@ -524,7 +524,8 @@ typedef struct hq_checkpoint {
  *   y    = fl32(fl32(h * rstd) * weight)       (no product without a weight)
  *   q, scale_out = the per-token quantization of y, as hq_quantize_fp8
  * h is used unrounded; a NaN in a row makes the row's codes 0x7F, an Inf makes
- * its own code 0x7F and the row's others 0.
+ * its own code 0x7F and the row's others 0; squares whose sum passes float32's range
+ * make rstd and the row's codes 0.
  *   x          device, [rows, cols] of xt
  *   residual   device, [rows, cols] of xt, or NULL
  *   weight     device, [cols] of xt, or NULL for ones
@@ -661,7 +662,8 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
  * beside the result's own rounding). Otherwise it is carried as two f16 numbers,
  * exact to 2^-23 of a term or 2^-40 of the largest |g * x_scale| of its column n,
  * whichever is more, at twice the matrix-core work.
- * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n, m * k and n * k < 2^40; 16-byte aligned g, xq, base, dw; no output may overlap an input
+ * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n and m * k < 2^40,
+ * n * k < 2^38; 16-byte aligned g, xq, base, dw; no output may overlap an input
  * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
  * base, or zeros. */
 hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
