@@ -179,9 +179,9 @@ __device__ __forceinline__ void act_bwd_vec(const uint4& dav, const uint32_t* w1
 // thread keeps its columns' sums of dz in registers (unrounded), the row groups
 // meet in LDS at the end, and one partial row per workgroup goes to the
 // workspace for column_sums_kernel. dz goes through the caches: 8192 x 4096 bf16 SiLU
-// gated (271 MB, 52.6 us at a large copy's 5.15 TB/s) takes 49.1 us replayed from a
-// graph, 55.5 with dz streamed past them and two workgroups per CU; 52.6 with runs of
-// neighbouring rows per workgroup.
+// gated (271 MB, 44.0 us at 6.15 TB/s, a large elementwise pass's best) takes 49.1 us
+// replayed from a graph, 45.4 of it this kernel; 55.5 with dz streamed past them and
+// two workgroups per CU; 52.6 with runs of neighbouring rows per workgroup.
 template <int XT, int CW, int ACT, bool GATED>
 __global__ __launch_bounds__(1024) void act_bwd_kernel(ActBwdArgs a) {
   constexpr int E = VecTraits<XT>::kElems;

@@ -226,9 +226,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
 // the workspace, which column_sums_kernel adds in order: dw does not depend on
 // which workgroup ends first. dx goes through the caches (the next kernel reads
 // it): streamed past them it took 49.3 us instead of 45.6 at 8192 x 4096 bf16 with a
-// checkpoint. That shape moves 236 MB, 45.8 us at a large copy's 5.15 TB/s; more
-// workgroups per CU (51 to 63 us for 2 to 8), loading the next row ahead (49.5, before
-// the stores changed) and runs of neighbouring rows per workgroup (49.1) were slower.
+// checkpoint (40.8 of it this kernel). That shape moves 236 MB, 38.4 us at 6.15 TB/s, a
+// large elementwise pass's best; more workgroups per CU (51 to 63 us for 2 to 8),
+// loading the next row ahead (49.5, before the stores changed) and runs of neighbouring
+// rows per workgroup (49.1) were slower.
 constexpr int kBwdLdsFloats = 16384;
 
 // Few rows: dw needs nothing that dx computes (rstd is given), so the same launch
