@@ -362,19 +362,41 @@ def hq_quantize_fp8_preshuffled(x: torch.Tensor, fmt: int = HQ_E4M3, *, row_majo
     return q_pre, scale_out, amax_out, q
 
 
-_GEMM_WORKSPACE = {}
+_GEMM_WORKSPACE = {}     # (device, stream) -> buffer of the calls outside captures
+_CAPTURE_WORKSPACE = {}  # (device, stream) -> (capture, buffer) of its latest capture
+
+
+def _capture_id(stream: int) -> int:
+    """Number of the graph capture that the stream (handle) is part of, 0 for none."""
+    return _native().capture_id(stream)
 
 
 def gemm_workspace(device, nbytes: int) -> torch.Tensor | None:
     """A GEMM workspace of at least `nbytes` for `device` and torch's current
     stream, zero-filled on that stream when made and kept for reuse (the
     kernels leave its counters at zero). Launches on one stream are ordered,
-    so they may share it; each stream gets its own."""
+    so they may share it; each stream gets its own.
+
+    Under graph capture the buffer belongs to that capture: it comes from the
+    graph's pool, its fill is part of the graph, and no call outside the capture
+    sees it. (A buffer shared with other calls would have counters that nothing
+    zeroes until the graph's first replay, two graphs replayed on different
+    streams would count in the same words, and one that a later call outgrows
+    would be freed while the graph still writes to it.)"""
     if nbytes <= 0:
         return None
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
-    key = (dev.type, idx, torch.cuda.current_stream(idx).cuda_stream)
+    stream = torch.cuda.current_stream(idx).cuda_stream
+    key = (dev.type, idx, stream)
+    capture = _capture_id(stream)
+    if capture:
+        owner, ws = _CAPTURE_WORKSPACE.get(key, (0, None))
+        if owner != capture or ws.numel() < nbytes:
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+            _CAPTURE_WORKSPACE[key] = (capture, ws)
+        return ws
+    _CAPTURE_WORKSPACE.pop(key, None)  # a capture that has ended; its graph's pool keeps the memory
     ws = _GEMM_WORKSPACE.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)

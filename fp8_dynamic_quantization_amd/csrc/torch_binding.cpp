@@ -325,6 +325,20 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// stream handle -> the number of the capture that it is part of, 0 for none
+PyObject* capture_id(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 1);
+  const hipStream_t st = reinterpret_cast<hipStream_t>(integer(a[0]));
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  const hipError_t e = hipStreamGetCaptureInfo(st, &status, &id);
+  if (e != hipSuccess) (void)hipGetLastError();
+  TORCH_CHECK(e == hipSuccess, "hipStreamGetCaptureInfo: ", hipGetErrorString(e));
+  return PyLong_FromUnsignedLongLong(status == hipStreamCaptureStatusNone ? 0 : id);
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 2);
@@ -338,7 +352,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define HQ_METHOD(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(F)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {HQ_METHOD(setup),        HQ_METHOD(rmsnorm_quantize), HQ_METHOD(rmsnorm_backward), HQ_METHOD(gemm_fused),
-                         HQ_METHOD(act_quantize), HQ_METHOD(act_backward),     HQ_METHOD(wgrad),            {nullptr, nullptr, 0, nullptr}};
+                         HQ_METHOD(act_quantize), HQ_METHOD(act_backward),     HQ_METHOD(wgrad),            HQ_METHOD(capture_id),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hqtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
