@@ -91,6 +91,15 @@ T* ptr(const Tensor& t) {
 
 hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
 
+// The caller's workspace, checked like an output's buffer: its bytes go to the kernels.
+Tensor workspace(PyObject* o, const Tensor& like) {
+  const Tensor t = maybe(o, "workspace");
+  if (!t.defined()) return t;
+  TORCH_CHECK_VALUE(t.device() == like.device(), "workspace must be on ", like.device(), ", got ", t.device());
+  TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous");
+  return t;
+}
+
 // Scratch without an initial value, from the caching allocator: its reuse is
 // ordered on the current stream, and under graph capture it belongs to the graph.
 Tensor scratch(const Tensor& given, bool allocate, size_t bytes, const Tensor& like) {
@@ -191,12 +200,13 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor w = input(maybe(a[5], "weight"), {cols}, dt, dy, "weight");
   const Tensor rstd = input(tensor(a[6], "rstd"), {rows}, ScalarType::Float, dy, "rstd");
   const Tensor dr = input(maybe(a[7], "dresidual"), {rows, cols}, dt, dy, "dresidual");
+  const Tensor given = workspace(a[11], dy);
   const c10::OptionalDeviceGuard guard(dy.device());
   const Tensor dx = output(maybe(a[8], "dx"), {rows, cols}, dt, dy, "dx");
   const bool sum = a[10] == Py_True;
   const Tensor dw = sum ? output(maybe(a[9], "dweight"), {cols}, ScalarType::Float, dy, "dweight") : Tensor();
   on_gpu(dy, "dy");
-  const Tensor ws = scratch(maybe(a[11], "workspace"), sum, hq_rmsnorm_backward_workspace_bytes(xt, rows, cols), dy);
+  const Tensor ws = scratch(given, sum, hq_rmsnorm_backward_workspace_bytes(xt, rows, cols), dy);
   raise_unless_ok(hq_rmsnorm_backward(ptr(dy), ptr(h), k.p(), ptr(w), ptr<float>(rstd), ptr(dr), xt, rows, cols, ptr(dx),
                                       ptr<float>(dw), ptr(ws), bytes_of(ws), stream_of(dy)));
   return wrap_all(dx, dw);
@@ -229,10 +239,10 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor bs = input(maybe(a[9], "bias_scale"), {1}, ScalarType::Float, xq, "bias_scale");
   const Tensor res = input(maybe(a[11], "residual"), {m, n}, ScalarType::BFloat16, xq, "residual");
   const Tensor os = input(maybe(a[12], "out_scale"), {1}, ScalarType::Float, xq, "out_scale");
+  Tensor work = a[15] == Py_False ? Tensor() : workspace(a[15], xq);
   const c10::OptionalDeviceGuard guard(xq.device());
   const Tensor out = output(maybe(a[14], "out"), {m, n}, os.defined() ? ScalarType::Byte : ScalarType::BFloat16, xq, "out");
   on_gpu(xq, "xq");
-  Tensor work;
   if (a[15] == Py_None) {
     const int64_t need = m <= 16 ? hq_gemm_workspace_bytes(m, n, k) : 0;  // more rows use none
     if (need > 0) {
@@ -241,8 +251,6 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       if (!r) throw python_error();
       work = tensor(r.get(), "workspace");
     }
-  } else if (a[15] != Py_False) {
-    work = tensor(a[15], "workspace");
   }
   const hq_fused_epilogue ep = {ptr(bias), (int32_t)bias_type, ptr<float>(bs), ptr<float>(os), (int32_t)integer(a[13]),
                                 (int32_t)integer(a[10]), ptr<uint16_t>(res)};
@@ -286,12 +294,13 @@ PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t rows = da.size(0), cols = da.size(1), wide = gated ? 2 * cols : cols, bs = integer(a[3]);
   TORCH_CHECK_VALUE(bs != 0, "z must be a checkpoint");
   const Ckpt k = checkpoint_in(a[1], a[2], bs, rows, wide, da);
+  const Tensor given = workspace(a[9], da);
   const c10::OptionalDeviceGuard guard(da.device());
   const Tensor dz = output(maybe(a[6], "dz"), {rows, wide}, da.scalar_type(), da, "dz");
   const bool sum = a[8] == Py_True;
   const Tensor db = sum ? output(maybe(a[7], "dbias"), {wide}, ScalarType::Float, da, "dbias") : Tensor();
   on_gpu(da, "da");
-  const Tensor ws = scratch(maybe(a[9], "workspace"), sum, hq_act_backward_workspace_bytes(xt, rows, cols, gated), da);
+  const Tensor ws = scratch(given, sum, hq_act_backward_workspace_bytes(xt, rows, cols, gated), da);
   raise_unless_ok(hq_act_backward(ptr(da), k.p(), xt, rows, cols, (int)integer(a[4]), gated, ptr(dz), ptr<float>(db),
                                   ptr(ws), bytes_of(ws), stream_of(da)));
   return wrap_all(dz, db);
@@ -312,13 +321,13 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const int64_t k = xq.size(1);
   const int dwt = (int)integer(a[4]);
   const Tensor base = input(maybe(a[5], "base"), {n, k}, ScalarType::Float, g, "base");
+  const Tensor given = a[7] == Py_False ? Tensor() : workspace(a[7], g);
   const c10::OptionalDeviceGuard guard(g.device());
   const Tensor dw = output(maybe(a[6], "dw"), {n, k}, dwt == HQ_F32 ? ScalarType::Float : ScalarType::BFloat16, g, "dw");
   on_gpu(g, "g");
   const bool allocate = a[7] == Py_None;
   const int64_t need = allocate ? hq_wgrad_workspace_bytes(m, n, k, dwt) : 0;
-  const Tensor ws = scratch(allocate || a[7] == Py_False ? Tensor() : tensor(a[7], "workspace"), allocate,
-                            need > 0 ? (size_t)need : 0, g);
+  const Tensor ws = scratch(given, allocate, need > 0 ? (size_t)need : 0, g);
   raise_unless_ok(hq_wgrad_a8(ptr<uint16_t>(g), ptr<uint8_t>(xq), (int)integer(a[2]), ptr<float>(xs), xs.numel(), m, n, k,
                               ptr<float>(base), ptr(dw), dwt, ptr(ws), bytes_of(ws), stream_of(g)));
   return wrap(dw);
