@@ -10,6 +10,10 @@
 // Arguments are positional and complete (api.py has the keywords and defaults);
 // None stands for a tensor that is not given. Refusals raise ValueError, and
 // errors of the library go through _lib.check.
+//
+// Each function reads its Python arguments first and then gives up the interpreter
+// lock for the checks, copies, allocations and the call: a copy, an allocation or a
+// launch that waits for the device (a full queue, say) stops no other Python thread.
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
@@ -92,12 +96,10 @@ T* ptr(const Tensor& t) {
 hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
 
 // The caller's workspace, checked like an output's buffer: its bytes go to the kernels.
-Tensor workspace(PyObject* o, const Tensor& like) {
-  const Tensor t = maybe(o, "workspace");
-  if (!t.defined()) return t;
+void check_workspace(const Tensor& t, const Tensor& like) {
+  if (!t.defined()) return;
   TORCH_CHECK_VALUE(t.device() == like.device(), "workspace must be on ", like.device(), ", got ", t.device());
   TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous");
-  return t;
 }
 
 // Scratch without an initial value, from the caching allocator: its reuse is
@@ -126,21 +128,22 @@ struct Ckpt {
   hq_checkpoint c{};
   const hq_checkpoint* p() const { return c.block_size ? &c : nullptr; }
 };
-Ckpt checkpoint_in(PyObject* q, PyObject* s, int64_t bs, int64_t rows, int64_t cols, const Tensor& like) {
+Ckpt checkpoint_in(const Tensor& q, const Tensor& s, int64_t bs, int64_t rows, int64_t cols, const Tensor& like) {
   Ckpt k;
   if (bs == 0) return k;
   const int64_t nb = blocks(cols, bs);
-  k.q = input(tensor(q, "checkpoint.q"), {rows, cols}, ScalarType::Byte, like, "checkpoint.q");
-  k.scales = input(tensor(s, "checkpoint.scales"), {rows, nb}, ScalarType::Float, like, "checkpoint.scales");
+  TORCH_CHECK_VALUE(q.defined() && s.defined(), "a checkpoint's q and scales must be tensors");
+  k.q = input(q, {rows, cols}, ScalarType::Byte, like, "checkpoint.q");
+  k.scales = input(s, {rows, nb}, ScalarType::Float, like, "checkpoint.scales");
   k.c = {ptr<uint8_t>(k.q), ptr<float>(k.scales), (int32_t)bs};
   return k;
 }
-Ckpt checkpoint_out(PyObject* q, PyObject* s, int64_t bs, int64_t rows, int64_t cols, const Tensor& like) {
+Ckpt checkpoint_out(const Tensor& q, const Tensor& s, int64_t bs, int64_t rows, int64_t cols, const Tensor& like) {
   Ckpt k;
   if (bs == 0) return k;
   const int64_t nb = blocks(cols, bs);
-  k.q = output(maybe(q, "checkpoint.q"), {rows, cols}, ScalarType::Byte, like, "checkpoint.q");
-  k.scales = output(maybe(s, "checkpoint.scales"), {rows, nb}, ScalarType::Float, like, "checkpoint.scales");
+  k.q = output(q, {rows, cols}, ScalarType::Byte, like, "checkpoint.q");
+  k.scales = output(s, {rows, nb}, ScalarType::Float, like, "checkpoint.scales");
   k.c = {ptr<uint8_t>(k.q), ptr<float>(k.scales), (int32_t)bs};
   return k;
 }
@@ -158,6 +161,17 @@ PyObject* wrap_all(const Ts&... ts) {
   return r;
 }
 
+// Without the interpreter lock while it lives (exceptions take it back on their way).
+class NoGil {
+ public:
+  NoGil() : state_(PyEval_SaveThread()) {}
+  ~NoGil() { PyEval_RestoreThread(state_); }
+  NoGil(const NoGil&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 void want(Py_ssize_t got, Py_ssize_t n) { TORCH_CHECK_VALUE(got == n, "expected ", n, " arguments, got ", got); }
 
 // x, weight, eps, fmt, residual, h, write_h, ckpt q, ckpt scales, block_size, q, scale, rstd
@@ -165,22 +179,34 @@ void want(Py_ssize_t got, Py_ssize_t n) { TORCH_CHECK_VALUE(got == n, "expected 
 PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 13);
-  const Tensor x0 = tensor(a[0], "x");
-  const int xt = real_type(x0, "x");
-  const Tensor x = x0.contiguous();
-  const ScalarType dt = x.scalar_type();
-  const int64_t rows = x.size(0), cols = x.size(1);
-  const Tensor w = input(maybe(a[1], "weight"), {cols}, dt, x, "weight");
-  const Tensor res = input(maybe(a[4], "residual"), {rows, cols}, dt, x, "residual");
-  const c10::OptionalDeviceGuard guard(x.device());
-  const Tensor h = a[6] == Py_True ? output(maybe(a[5], "h"), {rows, cols}, dt, x, "h") : Tensor();
-  const Ckpt k = checkpoint_out(a[7], a[8], integer(a[9]), rows, cols, x);
-  const Tensor q = output(maybe(a[10], "q"), {rows, cols}, ScalarType::Byte, x, "q");
-  const Tensor s = output(maybe(a[11], "scale_out"), {rows}, ScalarType::Float, x, "scale_out");
-  const Tensor r = output(maybe(a[12], "rstd_out"), {rows}, ScalarType::Float, x, "rstd_out");
-  on_gpu(x, "x");
-  raise_unless_ok(hq_rmsnorm_quantize_fp8(ptr(x), ptr(res), ptr(w), xt, rows, cols, (float)real(a[2]), (int)integer(a[3]),
-                                          ptr<uint8_t>(q), ptr<float>(s), ptr(h), ptr<float>(r), k.p(), stream_of(x)));
+  const Tensor x0 = tensor(a[0], "x"), w0 = maybe(a[1], "weight"), res0 = maybe(a[4], "residual");
+  const float eps = (float)real(a[2]);
+  const int fmt = (int)integer(a[3]);
+  const bool write_h = a[6] == Py_True;
+  const int64_t block = integer(a[9]);
+  const Tensor cq = maybe(a[7], "checkpoint.q"), cs = maybe(a[8], "checkpoint.scales");
+  Tensor h = maybe(a[5], "h"), q = maybe(a[10], "q"), s = maybe(a[11], "scale_out"), r = maybe(a[12], "rstd_out");
+  Ckpt k;
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(x0, "x");
+    const Tensor x = x0.contiguous();
+    const ScalarType dt = x.scalar_type();
+    const int64_t rows = x.size(0), cols = x.size(1);
+    const Tensor w = input(w0, {cols}, dt, x, "weight");
+    const Tensor res = input(res0, {rows, cols}, dt, x, "residual");
+    const c10::OptionalDeviceGuard guard(x.device());
+    h = write_h ? output(h, {rows, cols}, dt, x, "h") : Tensor();
+    k = checkpoint_out(cq, cs, block, rows, cols, x);
+    q = output(q, {rows, cols}, ScalarType::Byte, x, "q");
+    s = output(s, {rows}, ScalarType::Float, x, "scale_out");
+    r = output(r, {rows}, ScalarType::Float, x, "rstd_out");
+    on_gpu(x, "x");
+    st = hq_rmsnorm_quantize_fp8(ptr(x), ptr(res), ptr(w), xt, rows, cols, eps, fmt, ptr<uint8_t>(q), ptr<float>(s), ptr(h),
+                                 ptr<float>(r), k.p(), stream_of(x));
+  }
+  raise_unless_ok(st);
   return wrap_all(q, s, h, r, k.q, k.scales);
   END_HANDLE_TH_ERRORS
 }
@@ -190,25 +216,34 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 12);
-  const Tensor dy0 = tensor(a[0], "dy");
-  const int xt = real_type(dy0, "dy");
-  const Tensor dy = dy0.contiguous();
-  const ScalarType dt = dy.scalar_type();
-  const int64_t rows = dy.size(0), cols = dy.size(1);
-  const Tensor h = input(maybe(a[1], "h"), {rows, cols}, dt, dy, "h");
-  const Ckpt k = checkpoint_in(a[2], a[3], integer(a[4]), rows, cols, dy);
-  const Tensor w = input(maybe(a[5], "weight"), {cols}, dt, dy, "weight");
-  const Tensor rstd = input(tensor(a[6], "rstd"), {rows}, ScalarType::Float, dy, "rstd");
-  const Tensor dr = input(maybe(a[7], "dresidual"), {rows, cols}, dt, dy, "dresidual");
-  const Tensor given = workspace(a[11], dy);
-  const c10::OptionalDeviceGuard guard(dy.device());
-  const Tensor dx = output(maybe(a[8], "dx"), {rows, cols}, dt, dy, "dx");
+  const Tensor dy0 = tensor(a[0], "dy"), h0 = maybe(a[1], "h"), w0 = maybe(a[5], "weight"), rstd0 = tensor(a[6], "rstd");
+  const Tensor dr0 = maybe(a[7], "dresidual"), given = maybe(a[11], "workspace");
+  const int64_t block = integer(a[4]);
+  const Tensor cq = maybe(a[2], "checkpoint.q"), cs = maybe(a[3], "checkpoint.scales");
   const bool sum = a[10] == Py_True;
-  const Tensor dw = sum ? output(maybe(a[9], "dweight"), {cols}, ScalarType::Float, dy, "dweight") : Tensor();
-  on_gpu(dy, "dy");
-  const Tensor ws = scratch(given, sum, hq_rmsnorm_backward_workspace_bytes(xt, rows, cols), dy);
-  raise_unless_ok(hq_rmsnorm_backward(ptr(dy), ptr(h), k.p(), ptr(w), ptr<float>(rstd), ptr(dr), xt, rows, cols, ptr(dx),
-                                      ptr<float>(dw), ptr(ws), bytes_of(ws), stream_of(dy)));
+  Tensor dx = maybe(a[8], "dx"), dw = maybe(a[9], "dweight");
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(dy0, "dy");
+    const Tensor dy = dy0.contiguous();
+    const ScalarType dt = dy.scalar_type();
+    const int64_t rows = dy.size(0), cols = dy.size(1);
+    const Tensor h = input(h0, {rows, cols}, dt, dy, "h");
+    const Ckpt k = checkpoint_in(cq, cs, block, rows, cols, dy);
+    const Tensor w = input(w0, {cols}, dt, dy, "weight");
+    const Tensor rstd = input(rstd0, {rows}, ScalarType::Float, dy, "rstd");
+    const Tensor dr = input(dr0, {rows, cols}, dt, dy, "dresidual");
+    check_workspace(given, dy);
+    const c10::OptionalDeviceGuard guard(dy.device());
+    dx = output(dx, {rows, cols}, dt, dy, "dx");
+    dw = sum ? output(dw, {cols}, ScalarType::Float, dy, "dweight") : Tensor();
+    on_gpu(dy, "dy");
+    const Tensor ws = scratch(given, sum, hq_rmsnorm_backward_workspace_bytes(xt, rows, cols), dy);
+    st = hq_rmsnorm_backward(ptr(dy), ptr(h), k.p(), ptr(w), ptr<float>(rstd), ptr(dr), xt, rows, cols, ptr(dx), ptr<float>(dw),
+                             ptr(ws), bytes_of(ws), stream_of(dy));
+  }
+  raise_unless_ok(st);
   return wrap_all(dx, dw);
   END_HANDLE_TH_ERRORS
 }
@@ -218,45 +253,56 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   want(nargs, 16);
-  const Tensor xq0 = tensor(a[0], "xq");
-  TORCH_CHECK_VALUE(xq0.dim() == 2 && xq0.scalar_type() == ScalarType::Byte, "xq must be uint8 codes [m, k]");
-  const Tensor xq = xq0.contiguous();
-  const int64_t m = xq.size(0), k = xq.size(1), n = integer(a[6]);
-  const Tensor wp = tensor(a[2], "wq_pre"), xs0 = tensor(a[4], "x_scale"), ws0 = tensor(a[5], "w_scale");
-  TORCH_CHECK_VALUE(wp.scalar_type() == ScalarType::Byte && wp.is_contiguous() && wp.numel() >= hq_preshuffled_bytes(n, k),
-                    "wq_pre must hold the pre-shuffled codes of a [", n, ", ", k, "] weight");
-  TORCH_CHECK_VALUE(wp.device() == xq.device(), "wq_pre must be on ", xq.device(), ", got ", wp.device());
-  const Tensor xs = input(xs0, xs0.sizes(), ScalarType::Float, xq, "x_scale");
-  const Tensor ws = input(ws0, ws0.sizes(), ScalarType::Float, xq, "w_scale");
-  const int64_t bias_type = integer(a[8]);
-  Tensor bias = maybe(a[7], "bias");
-  if (bias.defined()) {
-    TORCH_CHECK_VALUE(bias.numel() == n &&
-                          bias.scalar_type() == (bias_type == HQ_BIAS_BF16 ? ScalarType::BFloat16 : ScalarType::Byte),
-                      "bias must have n elements, bf16 or (as bias_type says) uint8 FP8 codes");
-    bias = input(bias, bias.sizes(), bias.scalar_type(), xq, "bias");
-  }
-  const Tensor bs = input(maybe(a[9], "bias_scale"), {1}, ScalarType::Float, xq, "bias_scale");
-  const Tensor res = input(maybe(a[11], "residual"), {m, n}, ScalarType::BFloat16, xq, "residual");
-  const Tensor os = input(maybe(a[12], "out_scale"), {1}, ScalarType::Float, xq, "out_scale");
-  Tensor work = a[15] == Py_False ? Tensor() : workspace(a[15], xq);
-  const c10::OptionalDeviceGuard guard(xq.device());
-  const Tensor out = output(maybe(a[14], "out"), {m, n}, os.defined() ? ScalarType::Byte : ScalarType::BFloat16, xq, "out");
-  on_gpu(xq, "xq");
-  if (a[15] == Py_None) {
-    const int64_t need = m <= 16 ? hq_gemm_workspace_bytes(m, n, k) : 0;  // more rows use none
-    if (need > 0) {
-      THPObjectPtr dev(THPDevice_New(xq.device()));
-      THPObjectPtr r(PyObject_CallFunction(g_gemm_workspace, "OL", dev.get(), (long long)need));
-      if (!r) throw python_error();
-      work = tensor(r.get(), "workspace");
+  const Tensor xq0 = tensor(a[0], "xq"), wp = tensor(a[2], "wq_pre"), xs0 = tensor(a[4], "x_scale"), ws0 = tensor(a[5], "w_scale");
+  const int xf = (int)integer(a[1]), wf = (int)integer(a[3]), act = (int)integer(a[10]), out_fmt = (int)integer(a[13]);
+  const int64_t n = integer(a[6]), bias_type = integer(a[8]);
+  const Tensor bias0 = maybe(a[7], "bias"), bs0 = maybe(a[9], "bias_scale"), res0 = maybe(a[11], "residual");
+  const Tensor os0 = maybe(a[12], "out_scale");
+  const bool shared = a[15] == Py_None;
+  Tensor work = a[15] == Py_False ? Tensor() : maybe(a[15], "workspace");
+  Tensor out = maybe(a[14], "out"), xq, xs, ws, bias, bs, res, os;
+  int64_t m, k, need = 0;
+  {
+    const NoGil nogil;
+    TORCH_CHECK_VALUE(xq0.dim() == 2 && xq0.scalar_type() == ScalarType::Byte, "xq must be uint8 codes [m, k]");
+    xq = xq0.contiguous();
+    m = xq.size(0);
+    k = xq.size(1);
+    TORCH_CHECK_VALUE(wp.scalar_type() == ScalarType::Byte && wp.is_contiguous() && wp.numel() >= hq_preshuffled_bytes(n, k),
+                      "wq_pre must hold the pre-shuffled codes of a [", n, ", ", k, "] weight");
+    TORCH_CHECK_VALUE(wp.device() == xq.device(), "wq_pre must be on ", xq.device(), ", got ", wp.device());
+    xs = input(xs0, xs0.sizes(), ScalarType::Float, xq, "x_scale");
+    ws = input(ws0, ws0.sizes(), ScalarType::Float, xq, "w_scale");
+    if (bias0.defined()) {
+      TORCH_CHECK_VALUE(bias0.numel() == n &&
+                            bias0.scalar_type() == (bias_type == HQ_BIAS_BF16 ? ScalarType::BFloat16 : ScalarType::Byte),
+                        "bias must have n elements, bf16 or (as bias_type says) uint8 FP8 codes");
+      bias = input(bias0, bias0.sizes(), bias0.scalar_type(), xq, "bias");
     }
+    bs = input(bs0, {1}, ScalarType::Float, xq, "bias_scale");
+    res = input(res0, {m, n}, ScalarType::BFloat16, xq, "residual");
+    os = input(os0, {1}, ScalarType::Float, xq, "out_scale");
+    check_workspace(work, xq);
+    const c10::OptionalDeviceGuard guard(xq.device());
+    out = output(out, {m, n}, os.defined() ? ScalarType::Byte : ScalarType::BFloat16, xq, "out");
+    on_gpu(xq, "xq");
+    if (shared && m <= 16) need = hq_gemm_workspace_bytes(m, n, k);  // more rows use none
   }
-  const hq_fused_epilogue ep = {ptr(bias), (int32_t)bias_type, ptr<float>(bs), ptr<float>(os), (int32_t)integer(a[13]),
-                                (int32_t)integer(a[10]), ptr<uint16_t>(res)};
-  raise_unless_ok(hq_gemm_a8w8_fused(ptr<uint8_t>(xq), (int)integer(a[1]), ptr<uint8_t>(wp), (int)integer(a[3]),
-                                     ptr<float>(xs), xs.numel(), ptr<float>(ws), ws.numel(), m, n, k, &ep, ptr(out),
-                                     ptr(work), bytes_of(work), stream_of(xq)));
+  const c10::OptionalDeviceGuard guard(xq.device());
+  if (need > 0) {
+    THPObjectPtr dev(THPDevice_New(xq.device()));
+    THPObjectPtr r(PyObject_CallFunction(g_gemm_workspace, "OL", dev.get(), (long long)need));
+    if (!r) throw python_error();
+    work = tensor(r.get(), "workspace");
+  }
+  hq_status st;
+  {
+    const NoGil nogil;
+    const hq_fused_epilogue ep = {ptr(bias), (int32_t)bias_type, ptr<float>(bs), ptr<float>(os), out_fmt, act, ptr<uint16_t>(res)};
+    st = hq_gemm_a8w8_fused(ptr<uint8_t>(xq), xf, ptr<uint8_t>(wp), wf, ptr<float>(xs), xs.numel(), ptr<float>(ws), ws.numel(), m,
+                            n, k, &ep, ptr(out), ptr(work), bytes_of(work), stream_of(xq));
+  }
+  raise_unless_ok(st);
   return wrap(out);
   END_HANDLE_TH_ERRORS
 }
@@ -266,19 +312,28 @@ PyObject* act_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 9);
   const Tensor z0 = tensor(a[0], "z");
-  const int xt = real_type(z0, "z");
-  const Tensor z = z0.contiguous();
+  const int act = (int)integer(a[1]), fmt = (int)integer(a[2]);
   const bool gated = a[3] == Py_True;
-  const int64_t rows = z.size(0), wide = z.size(1);
-  TORCH_CHECK_VALUE(!gated || wide % 2 == 0, "a gated z has an even number of columns");
-  const int64_t cols = gated ? wide / 2 : wide;
-  const c10::OptionalDeviceGuard guard(z.device());
-  const Ckpt k = checkpoint_out(a[4], a[5], integer(a[6]), rows, wide, z);
-  const Tensor q = output(maybe(a[7], "q"), {rows, cols}, ScalarType::Byte, z, "q");
-  const Tensor s = output(maybe(a[8], "scale_out"), {rows}, ScalarType::Float, z, "scale_out");
-  on_gpu(z, "z");
-  raise_unless_ok(hq_act_quantize_fp8(ptr(z), xt, rows, cols, (int)integer(a[1]), gated, (int)integer(a[2]), ptr<uint8_t>(q),
-                                      ptr<float>(s), k.p(), stream_of(z)));
+  const int64_t block = integer(a[6]);
+  const Tensor cq = maybe(a[4], "checkpoint.q"), cs = maybe(a[5], "checkpoint.scales");
+  Tensor q = maybe(a[7], "q"), s = maybe(a[8], "scale_out");
+  Ckpt k;
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(z0, "z");
+    const Tensor z = z0.contiguous();
+    const int64_t rows = z.size(0), wide = z.size(1);
+    TORCH_CHECK_VALUE(!gated || wide % 2 == 0, "a gated z has an even number of columns");
+    const int64_t cols = gated ? wide / 2 : wide;
+    const c10::OptionalDeviceGuard guard(z.device());
+    k = checkpoint_out(cq, cs, block, rows, wide, z);
+    q = output(q, {rows, cols}, ScalarType::Byte, z, "q");
+    s = output(s, {rows}, ScalarType::Float, z, "scale_out");
+    on_gpu(z, "z");
+    st = hq_act_quantize_fp8(ptr(z), xt, rows, cols, act, gated, fmt, ptr<uint8_t>(q), ptr<float>(s), k.p(), stream_of(z));
+  }
+  raise_unless_ok(st);
   return wrap_all(q, s, k.q, k.scales);
   END_HANDLE_TH_ERRORS
 }
@@ -287,22 +342,30 @@ PyObject* act_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 10);
-  const Tensor da0 = tensor(a[0], "da");
-  const int xt = real_type(da0, "da");
-  const Tensor da = da0.contiguous();
-  const bool gated = a[5] == Py_True;
-  const int64_t rows = da.size(0), cols = da.size(1), wide = gated ? 2 * cols : cols, bs = integer(a[3]);
-  TORCH_CHECK_VALUE(bs != 0, "z must be a checkpoint");
-  const Ckpt k = checkpoint_in(a[1], a[2], bs, rows, wide, da);
-  const Tensor given = workspace(a[9], da);
-  const c10::OptionalDeviceGuard guard(da.device());
-  const Tensor dz = output(maybe(a[6], "dz"), {rows, wide}, da.scalar_type(), da, "dz");
-  const bool sum = a[8] == Py_True;
-  const Tensor db = sum ? output(maybe(a[7], "dbias"), {wide}, ScalarType::Float, da, "dbias") : Tensor();
-  on_gpu(da, "da");
-  const Tensor ws = scratch(given, sum, hq_act_backward_workspace_bytes(xt, rows, cols, gated), da);
-  raise_unless_ok(hq_act_backward(ptr(da), k.p(), xt, rows, cols, (int)integer(a[4]), gated, ptr(dz), ptr<float>(db),
-                                  ptr(ws), bytes_of(ws), stream_of(da)));
+  const Tensor da0 = tensor(a[0], "da"), given = maybe(a[9], "workspace");
+  const int64_t block = integer(a[3]);
+  TORCH_CHECK_VALUE(block != 0, "z must be a checkpoint");
+  const Tensor cq = maybe(a[1], "checkpoint.q"), cs = maybe(a[2], "checkpoint.scales");
+  const int act = (int)integer(a[4]);
+  const bool gated = a[5] == Py_True, sum = a[8] == Py_True;
+  Tensor dz = maybe(a[6], "dz"), db = maybe(a[7], "dbias");
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(da0, "da");
+    const Tensor da = da0.contiguous();
+    const int64_t rows = da.size(0), cols = da.size(1), wide = gated ? 2 * cols : cols;
+    const Ckpt k = checkpoint_in(cq, cs, block, rows, wide, da);
+    check_workspace(given, da);
+    const c10::OptionalDeviceGuard guard(da.device());
+    dz = output(dz, {rows, wide}, da.scalar_type(), da, "dz");
+    db = sum ? output(db, {wide}, ScalarType::Float, da, "dbias") : Tensor();
+    on_gpu(da, "da");
+    const Tensor ws = scratch(given, sum, hq_act_backward_workspace_bytes(xt, rows, cols, gated), da);
+    st = hq_act_backward(ptr(da), k.p(), xt, rows, cols, act, gated, ptr(dz), ptr<float>(db), ptr(ws), bytes_of(ws),
+                         stream_of(da));
+  }
+  raise_unless_ok(st);
   return wrap_all(dz, db);
   END_HANDLE_TH_ERRORS
 }
@@ -311,25 +374,32 @@ PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   want(nargs, 8);
-  const Tensor g0 = tensor(a[0], "g"), xq0 = tensor(a[1], "xq"), xs0 = tensor(a[3], "x_scale");
-  TORCH_CHECK_VALUE(g0.dim() == 2 && g0.scalar_type() == ScalarType::BFloat16, "g must be a 2-D bfloat16 tensor [m, n]");
-  const Tensor g = g0.contiguous();
-  const int64_t m = g.size(0), n = g.size(1);
-  TORCH_CHECK_VALUE(xq0.dim() == 2 && xq0.size(0) == m, "xq must be uint8 codes [m, k]");
-  const Tensor xq = input(xq0, xq0.sizes(), ScalarType::Byte, g, "xq");
-  const Tensor xs = input(xs0, xs0.sizes(), ScalarType::Float, g, "x_scale");
-  const int64_t k = xq.size(1);
-  const int dwt = (int)integer(a[4]);
-  const Tensor base = input(maybe(a[5], "base"), {n, k}, ScalarType::Float, g, "base");
-  const Tensor given = a[7] == Py_False ? Tensor() : workspace(a[7], g);
-  const c10::OptionalDeviceGuard guard(g.device());
-  const Tensor dw = output(maybe(a[6], "dw"), {n, k}, dwt == HQ_F32 ? ScalarType::Float : ScalarType::BFloat16, g, "dw");
-  on_gpu(g, "g");
+  const Tensor g0 = tensor(a[0], "g"), xq0 = tensor(a[1], "xq"), xs0 = tensor(a[3], "x_scale"), base0 = maybe(a[5], "base");
+  const int xf = (int)integer(a[2]), dwt = (int)integer(a[4]);
   const bool allocate = a[7] == Py_None;
-  const int64_t need = allocate ? hq_wgrad_workspace_bytes(m, n, k, dwt) : 0;
-  const Tensor ws = scratch(given, allocate, need > 0 ? (size_t)need : 0, g);
-  raise_unless_ok(hq_wgrad_a8(ptr<uint16_t>(g), ptr<uint8_t>(xq), (int)integer(a[2]), ptr<float>(xs), xs.numel(), m, n, k,
-                              ptr<float>(base), ptr(dw), dwt, ptr(ws), bytes_of(ws), stream_of(g)));
+  const Tensor given = a[7] == Py_False ? Tensor() : maybe(a[7], "workspace");
+  Tensor dw = maybe(a[6], "dw");
+  hq_status st;
+  {
+    const NoGil nogil;
+    TORCH_CHECK_VALUE(g0.dim() == 2 && g0.scalar_type() == ScalarType::BFloat16, "g must be a 2-D bfloat16 tensor [m, n]");
+    const Tensor g = g0.contiguous();
+    const int64_t m = g.size(0), n = g.size(1);
+    TORCH_CHECK_VALUE(xq0.dim() == 2 && xq0.size(0) == m, "xq must be uint8 codes [m, k]");
+    const Tensor xq = input(xq0, xq0.sizes(), ScalarType::Byte, g, "xq");
+    const Tensor xs = input(xs0, xs0.sizes(), ScalarType::Float, g, "x_scale");
+    const int64_t k = xq.size(1);
+    const Tensor base = input(base0, {n, k}, ScalarType::Float, g, "base");
+    check_workspace(given, g);
+    const c10::OptionalDeviceGuard guard(g.device());
+    dw = output(dw, {n, k}, dwt == HQ_F32 ? ScalarType::Float : ScalarType::BFloat16, g, "dw");
+    on_gpu(g, "g");
+    const int64_t need = allocate ? hq_wgrad_workspace_bytes(m, n, k, dwt) : 0;
+    const Tensor ws = scratch(given, allocate, need > 0 ? (size_t)need : 0, g);
+    st = hq_wgrad_a8(ptr<uint16_t>(g), ptr<uint8_t>(xq), xf, ptr<float>(xs), xs.numel(), m, n, k, ptr<float>(base), ptr(dw), dwt,
+                     ptr(ws), bytes_of(ws), stream_of(g));
+  }
+  raise_unless_ok(st);
   return wrap(dw);
   END_HANDLE_TH_ERRORS
 }
