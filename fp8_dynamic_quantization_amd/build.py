@@ -75,20 +75,26 @@ def _link(cmd: list[str], out: str) -> None:
     os.replace(out + ".tmp", out)
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source and link libhq.so and the binding; returns the library path."""
+def _link_binding(obj: str) -> None:
     from torch.utils import cpp_extension
 
+    # torch's libraries are in the process already when the binding is imported
+    torch_lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
+    _link([os.environ.get("CXX", "g++"), "-shared", obj, f"-L{PKG}", "-l:libhq.so", f"-L{torch_lib}", "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], BINDING)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source and link libhq.so and the binding; returns the library path.
+
+    The C library needs neither torch nor a host compiler: it is linked before the
+    binding's object is waited for, so a failure there leaves it built (and raises)."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding = binding.result()
-    _link([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libhq.so", *objs], LIB)
-    # torch's libraries are in the process already when the binding is imported
-    torch_lib = os.path.join(os.path.dirname(cpp_extension.__file__), "..", "lib")
-    _link([os.environ.get("CXX", "g++"), "-shared", binding, f"-L{PKG}", "-l:libhq.so", f"-L{torch_lib}", "-lc10", "-lc10_hip",
-           "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], BINDING)
+        _link([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libhq.so", *objs], LIB)
+        _link_binding(binding.result())
     if verbose:
         print(f"built {LIB}")
     return LIB
