@@ -796,6 +796,10 @@ hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, i
 }
 
 // Sizes of the row operators; `wide` is the longest row among the call's tensors.
+static bool row_sizes(int xt, int64_t rows, int64_t cols, int64_t wide) {
+  return (xt == HQ_F32 || xt == HQ_BF16) && rows >= 0 && rows <= kMaxDim && cols >= 16 && cols % 16 == 0 && wide <= kMaxDim &&
+         (double)rows * (double)wide <= 1099511627776.0;
+}
 static hq_status check_rows(int xt, int64_t rows, int64_t cols, int64_t wide) {
   if (xt != HQ_F32 && xt != HQ_BF16) return fail(HQ_ERR_INVALID_ARGUMENT, "xt must be HQ_F32 or HQ_BF16, got %d", xt);
   if (rows < 0 || rows > kMaxDim)
@@ -867,7 +871,7 @@ hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const voi
 }
 
 size_t hq_rmsnorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols) {
-  if ((xt != HQ_F32 && xt != HQ_BF16) || rows < 1 || cols < 16 || cols % 16 != 0 || rows > kMaxDim || cols > kMaxDim) return 0;
+  if (!row_sizes(xt, rows, cols, cols) || rows == 0) return 0;
   return hq::rmsnorm_bwd_workspace_bytes((int)rows, (int)cols, xt);
 }
 
@@ -970,7 +974,7 @@ hq_status hq_act_quantize_fp8(const void* z, int xt, int64_t rows, int64_t cols,
 }
 
 size_t hq_act_backward_workspace_bytes(int xt, int64_t rows, int64_t cols, int gated) {
-  if ((xt != HQ_F32 && xt != HQ_BF16) || rows < 1 || cols < 16 || cols % 16 != 0 || rows > kMaxDim || cols > kMaxDim) return 0;
+  if ((gated != 0 && gated != 1) || cols > kMaxDim || !row_sizes(xt, rows, cols, gated ? 2 * cols : cols) || rows == 0) return 0;
   return hq::act_bwd_workspace_bytes((int)rows, (int)cols, xt, gated != 0);
 }
 

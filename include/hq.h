@@ -535,7 +535,7 @@ typedef struct hq_checkpoint {
  *   rstd_out   device, float32 [rows], or NULL (the backward pass needs it)
  *   ckpt       host pointer to an hq_checkpoint whose buffers receive h's 8-bit
  *              block-wise form, or NULL
- * Requires cols % 16 == 0, rows, cols <= 2^31 - 1024, rows * cols < 2^40, eps >= 0
+ * Requires cols % 16 == 0, rows, cols <= 2^31 - 1024, rows * cols <= 2^40, eps >= 0
  * and finite; no other overlap of an output with another buffer. rows == 0 returns
  * HQ_OK without a launch. Rows of up to 32768 bf16 (16384 float32) elements are
  * read once, longer ones three times. */
@@ -544,7 +544,7 @@ hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const voi
                                   float* rstd_out, const hq_checkpoint* ckpt, hipStream_t stream);
 
 /* Bytes of device workspace hq_rmsnorm_backward needs for dweight: partial sums
- * of at most 256 rows, [<= 256, cols] float32. 0 for invalid arguments. */
+ * of at most 256 rows, [<= 256, cols] float32. 0 for arguments that it refuses. */
 size_t hq_rmsnorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols);
 
 /* Backward pass of that norm. With xh = h * rstd and t = dy * weight:
@@ -610,15 +610,15 @@ hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, i
  *   q          device, uint8 [rows, cols]; scale_out device, float32 [rows]
  *   ckpt       host pointer to an hq_checkpoint to be written, or NULL
  * Requires cols % 16 == 0 and, gated with a checkpoint, cols % block_size == 0
- * (no block spans both halves); rows, 2 * cols <= 2^31 - 1024, rows * cols < 2^40;
- * no output may overlap another buffer. rows == 0 returns HQ_OK without a launch.
+ * (no block spans both halves); rows and the width of z <= 2^31 - 1024, elements of
+ * z <= 2^40; no output may overlap another buffer. rows == 0 returns HQ_OK without a launch.
  * Rows of up to 32768 bf16 (16384 float32) elements of `a` are read once, longer
  * ones twice. */
 hq_status hq_act_quantize_fp8(const void* z, int xt, int64_t rows, int64_t cols, int act, int gated, int fmt, uint8_t* q,
                               float* scale_out, const hq_checkpoint* ckpt, hipStream_t stream);
 
-/* Bytes of device workspace hq_act_backward needs for dbias. 0 for invalid
- * arguments. */
+/* Bytes of device workspace hq_act_backward needs for dbias. 0 for arguments that
+ * it refuses. */
 size_t hq_act_backward_workspace_bytes(int xt, int64_t rows, int64_t cols, int gated);
 
 /* Backward pass of that activation from the 8-bit checkpoint, z^ = dec(q) * scale:
