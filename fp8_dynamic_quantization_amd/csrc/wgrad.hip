@@ -15,15 +15,18 @@
 //
 // The FP8 codes are exact in bf16 and in f16 and are converted after the read. The
 // token's scale is folded into G on its way to LDS, once per workgroup. Two forms:
-//   one number   v = g * scale rounded to bf16, at most 2^-8 of a term: for a bf16
-//                result, whose own rounding is as large as what is left of the terms'
-//                after they are summed
+//   one number   v = g * scale[m] rounded to bf16, at most 2^-8 of a term: for a bf16
+//                result of many tokens, over which the roundings average (2048 normal
+//                tokens: 0.0016 of the result's norm beside 0.0017 from its own
+//                rounding; where a column's terms cancel, more of what is left). One
+//                scale for all tokens is applied to the sums instead: g and the codes
+//                are exact in bf16, and no term is rounded
 //   two numbers  v = hi + lo in f16, both multiplied (V_MFMA_F32_16X16X32_F16, the
 //                same rate): 2^-23 of a term. f16's range is covered by scaling each
 //                column of G by the power of two that takes the largest |g * scale|
 //                of the column below 2^15, undone on the sums (both exact); a term
-//                2^29 below its column's largest starts to lose bits, by 2^-40 of
-//                that largest. (Two bf16 numbers need no scaling but leave 2^-17 of a
+//                2^29 below its column's largest starts to lose bits, by 2^-39 of
+//                that largest (half of f16's smallest step, against 2^14 or more). (Two bf16 numbers need no scaling but leave 2^-17 of a
 //                term: 1.1e-6 of a result, against 6e-8 for float32 arithmetic.)
 //                For a float32 result, and for few tokens, which leave little to
 //                average the terms' roundings over.
@@ -141,10 +144,13 @@ __global__ __launch_bounds__(1024) void wgrad_colmax_kernel(WgradArgs a, int row
 //
 // Steps [step0, step1) of MS tokens; `part` selects the partial-sum slab when the
 // tokens are split over workgroups.
-template <int XF, int BN, int BK, int KS, int MS, bool HILO>
+// PER: the scale is read with each piece of G. The two-number form does so for one scale,
+// too, with a step of zero; the one-number form has an instance of its own for it.
+template <int XF, int BN, int BK, int KS, int MS, bool HILO, bool PER>
 __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, int tiles_k, int steps_per_part,
                                                     float* partials) {
   using C = WgCfg<BN, BK, KS, MS, HILO>;
+  static_assert(PER || !HILO, "two numbers read the scale with each piece");
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
   int tn, tk;
   tile_coords(xcd_remap(blockIdx.x, tiles_n * tiles_k), tiles_n, tiles_k, &tn, &tk);
@@ -168,6 +174,17 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   const __amdgpu_buffer_rsrc_t s_rsrc = row_rsrc(a.x_scale, a.x_scale_per_row ? (uint32_t)a.m * 4u : 4u);
   const int s_step = a.x_scale_per_row ? 4 : 0;  // bytes from a token's scale to the next one's
   constexpr int H = HILO ? 2 : 1;
+
+  // One scale for all tokens: its power of two is folded into G, which is exact, and the
+  // sums are multiplied by the rest, in [1, 2) (the power of two keeps the sums in the
+  // result's range). A scale that is zero, subnormal or not finite goes to the sums whole.
+  float fold = 1.0f, rest = 1.0f;
+  if (!PER && a.m > 0) {
+    const uint32_t b = __float_as_uint(a.x_scale[0]), p2 = b & kInfBits;
+    const bool normal = p2 != 0u && p2 != kInfBits;
+    fold = __uint_as_float(normal ? p2 : 0x3f800000u);
+    rest = __uint_as_float(normal ? (b & ~kInfBits) | 0x3f800000u : b);
+  }
 
   // Two numbers: the exponents of the tile's columns, from the maxima that a pass
   // before this one wrote, or from the tile's own columns.
@@ -241,16 +258,18 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   };
   auto load_g = [&](int v) {
     rg[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(g_rsrc, g_vo, (int)((uint32_t)(v * C::kGStep) * (uint32_t)a.n * 2u), 0));
-    rs[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_vo, v * C::kGStep * s_step, 0));
+    if constexpr (PER)
+      rs[v] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s_rsrc, s_vo, v * C::kGStep * s_step, 0));
   };
   auto load_x = [&](int v) {
     rx[v] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, x_vo, (int)((uint32_t)(v * C::kXStep) * (uint32_t)a.k), 0));
   };
   auto store_g = [&](uint8_t* stage, int v) {
     uint32_t hi[4], lo[4];
+    const float sc = PER ? rs[v] : fold;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * rs[v], vec_elem<kBF16>(rg[v], 2 * e + 1) * rs[v]};
+      f2v p = {vec_elem<kBF16>(rg[v], 2 * e) * sc, vec_elem<kBF16>(rg[v], 2 * e + 1) * sc};
       if constexpr (HILO) {
         const int* ex = s_exp + g_c * 8 + 2 * e;  // read at each use: registers are short
         p = f2v{__builtin_ldexpf(p[0], ex[0]), __builtin_ldexpf(p[1], ex[1])};
@@ -372,7 +391,7 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
   raw[0] = read_x(lds_g, 0);
   raw[1] = read_x(lds_g, 1);
   xb[0] = decode8<XF, HILO>(raw[0]);
-  if constexpr (kSub % 2 == 0) {
+  if constexpr (kSub % 2 == 0 && PER) {
     // two steps per iteration: the stages' offsets are constants
     for (int i = 0; i < iters; i += 2) {
       set_step();
@@ -382,8 +401,10 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
       step(1);
     }
   } else {
-    // one; its fragments of G are read after the step before's last MFMAs (reading them
-    // earlier into registers of their own took 256 registers and spilled)
+    // one. With one sub-step its fragments of G are read after the step before's last MFMAs
+    // (reading them earlier into registers of their own took 256 registers and spilled);
+    // with one scale for all tokens the product of the sums with it left the two-step
+    // loop's 256 x 256 tile 168 registers short (845 us at 4096^3)
     for (int i = 0; i < iters; ++i) {
       set_step();
       step(i & 1);
@@ -423,6 +444,10 @@ __global__ __launch_bounds__(512) void wgrad_kernel(WgradArgs a, int tiles_n, in
       if constexpr (HILO) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], back);
+      }
+      if constexpr (!PER) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= rest;
       }
       if (partials) {
         *reinterpret_cast<v4f*>(partials + (size_t)blockIdx.y * a.n * a.k + at) = v;
@@ -495,7 +520,7 @@ static WgPlan wgrad_plan(int m, int n, int k, bool out_f32) {
 
 size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32) { return wgrad_plan(m, n, k, out_f32).bytes; }
 
-template <int XF, bool HILO>
+template <int XF, bool HILO, bool PER>
 static hipError_t launch_wgrad_t(WgradArgs a, WgPlan p, uint8_t* workspace, size_t workspace_bytes, hipStream_t st) {
   constexpr int MS = HILO ? 32 : 64;
   float* partials = nullptr;
@@ -516,10 +541,10 @@ static hipError_t launch_wgrad_t(WgradArgs a, WgPlan p, uint8_t* workspace, size
   }
   const dim3 grid(p.tiles_n * p.tiles_k, p.parts);
   if (p.big)
-    hipLaunchKernelGGL((wgrad_kernel<XF, 256, 256, 1, MS, HILO>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
+    hipLaunchKernelGGL((wgrad_kernel<XF, 256, 256, 1, MS, HILO, PER>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
                        partials);
   else
-    hipLaunchKernelGGL((wgrad_kernel<XF, 128, 128, 2, MS, HILO>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
+    hipLaunchKernelGGL((wgrad_kernel<XF, 128, 128, 2, MS, HILO, PER>), grid, dim3(512), 0, st, a, p.tiles_n, p.tiles_k, p.steps,
                        partials);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !partials) return e;
@@ -529,13 +554,18 @@ static hipError_t launch_wgrad_t(WgradArgs a, WgPlan p, uint8_t* workspace, size
   return hipGetLastError();
 }
 
+template <int XF>
+static hipError_t launch_wgrad_x(const WgradArgs& a, const WgPlan& p, uint8_t* workspace, size_t workspace_bytes, hipStream_t st) {
+  if (p.hilo) return launch_wgrad_t<XF, true, true>(a, p, workspace, workspace_bytes, st);
+  return a.x_scale_per_row ? launch_wgrad_t<XF, false, true>(a, p, workspace, workspace_bytes, st)
+                           : launch_wgrad_t<XF, false, false>(a, p, workspace, workspace_bytes, st);
+}
+
 hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st) {
   const WgPlan p = wgrad_plan(a.m, a.n, a.k, a.out_f32);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (xf == kE4M3) return p.hilo ? launch_wgrad_t<kE4M3, true>(a, p, ws, workspace_bytes, st)
-                                 : launch_wgrad_t<kE4M3, false>(a, p, ws, workspace_bytes, st);
-  return p.hilo ? launch_wgrad_t<kE5M2, true>(a, p, ws, workspace_bytes, st)
-                : launch_wgrad_t<kE5M2, false>(a, p, ws, workspace_bytes, st);
+  return xf == kE4M3 ? launch_wgrad_x<kE4M3>(a, p, ws, workspace_bytes, st)
+                     : launch_wgrad_x<kE5M2>(a, p, ws, workspace_bytes, st);
 }
 
 }  // namespace hq

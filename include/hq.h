@@ -658,10 +658,12 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
  *              call is slower, and its sums may be associated otherwise. Calls that
  *              share one must not run concurrently
  * Products run on the 16-bit matrix cores with float32 sums. For a bf16 result of
- * more than 64 tokens g * x_scale[m] is rounded to bf16 (at most 2^-8 of a term,
- * beside the result's own rounding). Otherwise it is carried as two f16 numbers,
- * exact to 2^-23 of a term or 2^-40 of the largest |g * x_scale| of its column n,
- * whichever is more, at twice the matrix-core work.
+ * more than 64 tokens with a scale per token, g * x_scale[m] is rounded to bf16 (at
+ * most 2^-8 of a term: a column whose terms cancel loses that of its terms, not of
+ * what is left); one scale for all tokens is applied to the sums, and no term is
+ * rounded. Otherwise g * x_scale[m] is carried as two f16 numbers, exact to 2^-23 of
+ * a term or 2^-39 of the largest |g * x_scale| of its column n, whichever is more, at
+ * twice the matrix-core work.
  * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n and m * k < 2^40,
  * n * k < 2^38; 16-byte aligned g, xq, base, dw; no output may overlap an input
  * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
