@@ -9,7 +9,7 @@ from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_A
                    HQUnsupportedDevice, LIB_PATH, SIGNATURES, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_ring, load)
 from .api import (Checkpoint, RmsNormQuantized, Ring, hq_act_backward, hq_act_backward_workspace_bytes, hq_act_quantize_fp8,
                   hq_gemm_a8w8_fused, hq_rmsnorm_backward, hq_rmsnorm_backward_workspace_bytes, hq_rmsnorm_quantize_fp8,
-                  hq_wgrad_a8, hq_wgrad_workspace_bytes, gemm_workspace, hq_gemm_a8w8, hq_gemm_a8w8_blockscaled, hq_gemm_a8w8_epilogue,
+                  hq_wgrad_a8, hq_wgrad_a8_strict, hq_wgrad_workspace_bytes, gemm_workspace, hq_gemm_a8w8, hq_gemm_a8w8_blockscaled, hq_gemm_a8w8_epilogue,
                   hq_gemm_a8w8_blockscaled_preshuffled,
                   hq_gemm_workspace_bytes, hq_quantize_fp8_blockwise, hq_grouped_gemm_a8w8,
                   hq_grouped_gemm_a8w8_epilogue, hq_quantize_fp8_preshuffled, hq_gemm_a8w8_strict,
@@ -34,5 +34,5 @@ __all__ = [
     "HQ_ACT_NONE", "HQ_ACT_RELU", "HQ_ACT_GELU", "HQ_ACT_GELU_TANH", "HQ_ACT_SILU", "Checkpoint", "RmsNormQuantized",
     "hq_checkpoint", "hq_fused_epilogue", "hq_rmsnorm_quantize_fp8", "hq_rmsnorm_backward",
     "hq_rmsnorm_backward_workspace_bytes", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward",
-    "hq_act_backward_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_workspace_bytes",
+    "hq_act_backward_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict", "hq_wgrad_workspace_bytes",
 ]

@@ -124,6 +124,7 @@ SIGNATURES = {
     "hq_act_backward": (_I, [_P, ctypes.POINTER(hq_checkpoint), _I, _I64, _I64, _I, _I, _P, _P, _P, _SZ, _P]),
     "hq_wgrad_workspace_bytes": (_I64, [_I64, _I64, _I64, _I]),
     "hq_wgrad_a8": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
+    "hq_wgrad_a8_strict": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
     "hq_last_error": (ctypes.c_char_p, []),
 }
 

@@ -32,7 +32,7 @@ __all__ = [
     "hq_quantize_workspace_status", "hq_stream_rows_probe",
     "Checkpoint", "RmsNormQuantized", "hq_rmsnorm_quantize_fp8", "hq_rmsnorm_backward_workspace_bytes",
     "hq_rmsnorm_backward", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward_workspace_bytes",
-    "hq_act_backward", "hq_wgrad_workspace_bytes", "hq_wgrad_a8",
+    "hq_act_backward", "hq_wgrad_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict",
 ]
 
 _XT = {torch.float32: HQ_F32, torch.bfloat16: HQ_BF16}
@@ -700,15 +700,20 @@ def hq_wgrad_workspace_bytes(m: int, n: int, k: int, dwt: int) -> int:
 
 
 def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
-                base: torch.Tensor | None = None, dw=None, workspace=None, stream=None) -> torch.Tensor:
+                base: torch.Tensor | None = None, dw=None, workspace=None, stream=None, strict: bool = False) -> torch.Tensor:
     """dw[n, k] = base + sum_m g[m, n] x_scale[m] dec(xq[m, k]) from a bf16 gradient
     g [m, n] and the codes xq [m, k] that the forward GEMM read; dw of `dtype`
     (bfloat16 or float32; a float32 base only with float32, and dw may be base).
     `workspace`: None (allocated where the shape wants one), False (none) or a uint8
-    tensor."""
+    tensor. `strict`: no g * x_scale[m] is rounded to bf16 (hq_wgrad_a8_strict)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return hq_wgrad_a8(g, xq, xf, x_scale, dtype=dtype, base=base, dw=dw, workspace=workspace)
+            return hq_wgrad_a8(g, xq, xf, x_scale, dtype=dtype, base=base, dw=dw, workspace=workspace, strict=strict)
     if dtype not in _XT:
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
-    return _native().wgrad(g, xq, xf, x_scale, _XT[dtype], base, dw, workspace)
+    return _native().wgrad(g, xq, xf, x_scale, _XT[dtype], base, dw, workspace, bool(strict))
+
+
+def hq_wgrad_a8_strict(*args, **kwargs) -> torch.Tensor:
+    """hq_wgrad_a8 with every term in two numbers, whatever the result's type; same arguments."""
+    return hq_wgrad_a8(*args, strict=True, **kwargs)

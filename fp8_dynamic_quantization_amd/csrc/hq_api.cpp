@@ -1028,9 +1028,9 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt) {
   return (int64_t)hq::wgrad_workspace_bytes((int)m, (int)n, (int)k, dwt == HQ_F32);
 }
 
-hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
-                      int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
-                      size_t workspace_bytes, hipStream_t stream) {
+static hq_status wgrad_impl(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                            int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                            size_t workspace_bytes, bool strict, const char* name, hipStream_t stream) {
   if (!valid_fmt(xf)) return fail(HQ_ERR_INVALID_ARGUMENT, "xf must be HQ_E4M3 or HQ_E5M2, got %d", xf);
   if (dwt != HQ_BF16 && dwt != HQ_F32) return fail(HQ_ERR_INVALID_ARGUMENT, "dwt must be HQ_F32 or HQ_BF16, got %d", dwt);
   if (!wgrad_sizes(m, n, k))
@@ -1063,8 +1063,22 @@ hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float*
   st = check_device();
   if (st != HQ_OK) return st;
   (void)hipGetLastError();
-  const hq::WgradArgs a{g, xq, x_scale, base, dw, (int)m, (int)n, (int)k, x_scale_count != 1, dwt == HQ_F32};
-  return launched(hq::launch_wgrad(a, xf, workspace_bytes ? workspace : nullptr, workspace_bytes, stream), "hq_wgrad_a8");
+  const hq::WgradArgs a{g, xq, x_scale, base, dw, (int)m, (int)n, (int)k, x_scale_count != 1, dwt == HQ_F32, strict};
+  return launched(hq::launch_wgrad(a, xf, workspace_bytes ? workspace : nullptr, workspace_bytes, stream), name);
+}
+
+hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                      int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  return wgrad_impl(g, xq, xf, x_scale, x_scale_count, m, n, k, base, dw, dwt, workspace, workspace_bytes, false,
+                    "hq_wgrad_a8", stream);
+}
+
+hq_status hq_wgrad_a8_strict(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                             int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  return wgrad_impl(g, xq, xf, x_scale, x_scale_count, m, n, k, base, dw, dwt, workspace, workspace_bytes, true,
+                    "hq_wgrad_a8_strict", stream);
 }
 
 }  // extern "C"

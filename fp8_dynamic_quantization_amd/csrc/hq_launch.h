@@ -229,12 +229,13 @@ struct WgradArgs {
   void* dw;              // [n, k], bf16 or float32
   int m, n, k;
   int x_scale_per_row, out_f32;
+  int strict;  // two numbers per term whatever the result
   // Largest |g * scale| per column of g as float32 bits, [colmax_parts, n] (the
   // launcher sets them; null: each workgroup finds its own columns').
   const uint32_t* colmax;
   int colmax_parts;
 };
-size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32);
+size_t wgrad_workspace_bytes(int m, int n, int k, bool two_numbers);
 hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st);
 
 }  // namespace hq

@@ -370,13 +370,13 @@ PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// g, xq, xf, x_scale, dwt, base, dw, workspace (None: allocate, False: none) -> dw
+// g, xq, xf, x_scale, dwt, base, dw, workspace (None: allocate, False: none), strict -> dw
 PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
-  want(nargs, 8);
+  want(nargs, 9);
   const Tensor g0 = tensor(a[0], "g"), xq0 = tensor(a[1], "xq"), xs0 = tensor(a[3], "x_scale"), base0 = maybe(a[5], "base");
   const int xf = (int)integer(a[2]), dwt = (int)integer(a[4]);
-  const bool allocate = a[7] == Py_None;
+  const bool allocate = a[7] == Py_None, strict = a[8] == Py_True;
   const Tensor given = a[7] == Py_False ? Tensor() : maybe(a[7], "workspace");
   Tensor dw = maybe(a[6], "dw");
   hq_status st;
@@ -394,10 +394,10 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const c10::OptionalDeviceGuard guard(g.device());
     dw = output(dw, {n, k}, dwt == HQ_F32 ? ScalarType::Float : ScalarType::BFloat16, g, "dw");
     on_gpu(g, "g");
-    const int64_t need = allocate ? hq_wgrad_workspace_bytes(m, n, k, dwt) : 0;
+    const int64_t need = allocate ? hq_wgrad_workspace_bytes(m, n, k, strict ? (int)HQ_F32 : dwt) : 0;
     const Tensor ws = scratch(given, allocate, need > 0 ? (size_t)need : 0, g);
-    st = hq_wgrad_a8(ptr<uint16_t>(g), ptr<uint8_t>(xq), xf, ptr<float>(xs), xs.numel(), m, n, k, ptr<float>(base), ptr(dw), dwt,
-                     ptr(ws), bytes_of(ws), stream_of(g));
+    st = (strict ? hq_wgrad_a8_strict : hq_wgrad_a8)(ptr<uint16_t>(g), ptr<uint8_t>(xq), xf, ptr<float>(xs), xs.numel(), m, n, k,
+                                                     ptr<float>(base), ptr(dw), dwt, ptr(ws), bytes_of(ws), stream_of(g));
   }
   raise_unless_ok(st);
   return wrap(dw);

@@ -28,8 +28,9 @@
 //                2^29 below its column's largest starts to lose bits, by 2^-39 of
 //                that largest (half of f16's smallest step, against 2^14 or more). (Two bf16 numbers need no scaling but leave 2^-17 of a
 //                term: 1.1e-6 of a result, against 6e-8 for float32 arithmetic.)
-//                For a float32 result, and for few tokens, which leave little to
-//                average the terms' roundings over.
+//                For a float32 result, for few tokens, which leave little to average
+//                the terms' roundings over, and where the caller asks for it
+//                (2048 x 4096 x 1024 bf16 50 us against 25).
 #include "gemm_kernels.h"
 #include "hq_row.h"
 
@@ -496,9 +497,9 @@ struct WgPlan {
   int tiles_n, tiles_k, steps, parts, max_parts;
   size_t max_bytes, bytes;
 };
-static WgPlan wgrad_plan(int m, int n, int k, bool out_f32) {
+static WgPlan wgrad_plan(int m, int n, int k, bool two_numbers) {
   WgPlan p{};
-  p.hilo = out_f32 || m <= kWgTwoNumbersM;
+  p.hilo = two_numbers || m <= kWgTwoNumbersM;
   const int ms = p.hilo ? 32 : 64;
   auto tiles = [&](int b) { return (int64_t)((n + b - 1) / b) * ((k + b - 1) / b); };
   p.big = tiles(256) >= kNumCUs * 3 / 4;
@@ -518,7 +519,7 @@ static WgPlan wgrad_plan(int m, int n, int k, bool out_f32) {
   return p;
 }
 
-size_t wgrad_workspace_bytes(int m, int n, int k, bool out_f32) { return wgrad_plan(m, n, k, out_f32).bytes; }
+size_t wgrad_workspace_bytes(int m, int n, int k, bool two_numbers) { return wgrad_plan(m, n, k, two_numbers).bytes; }
 
 template <int XF, bool HILO, bool PER>
 static hipError_t launch_wgrad_t(WgradArgs a, WgPlan p, uint8_t* workspace, size_t workspace_bytes, hipStream_t st) {
@@ -562,7 +563,7 @@ static hipError_t launch_wgrad_x(const WgradArgs& a, const WgPlan& p, uint8_t* w
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, int xf, void* workspace, size_t workspace_bytes, hipStream_t st) {
-  const WgPlan p = wgrad_plan(a.m, a.n, a.k, a.out_f32);
+  const WgPlan p = wgrad_plan(a.m, a.n, a.k, a.out_f32 || a.strict);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   return xf == kE4M3 ? launch_wgrad_x<kE4M3>(a, p, ws, workspace_bytes, st)
                      : launch_wgrad_x<kE5M2>(a, p, ws, workspace_bytes, st);

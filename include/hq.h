@@ -663,7 +663,7 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
  * what is left); one scale for all tokens is applied to the sums, and no term is
  * rounded. Otherwise g * x_scale[m] is carried as two f16 numbers, exact to 2^-23 of
  * a term or 2^-39 of the largest |g * x_scale| of its column n, whichever is more, at
- * twice the matrix-core work.
+ * twice the matrix-core work; hq_wgrad_a8_strict does so for every result.
  * Requires n % 8 == 0, k % 16 == 0, m < 2^28, n, k < 2^24, m * n and m * k < 2^40,
  * n * k < 2^38; 16-byte aligned g, xq, base, dw; no output may overlap an input
  * other than as said. n == 0 or k == 0 returns HQ_OK without a launch; m == 0 writes
@@ -671,6 +671,13 @@ int64_t hq_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int dwt);
 hq_status hq_wgrad_a8(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
                       int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
                       size_t workspace_bytes, hipStream_t stream);
+
+/* hq_wgrad_a8 with every g * x_scale[m] in two numbers, also for a bf16 result of
+ * more than 64 tokens (a result that cancels, or a reference run). Its full workspace
+ * is hq_wgrad_workspace_bytes(m, n, k, HQ_F32) for either type of dw. */
+hq_status hq_wgrad_a8_strict(const uint16_t* g, const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count,
+                             int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
 
 /* Row-streaming probe: a measurement aid, not a step of the quantization (no
  * page defines it). It moves the bytes of a per-token quantize pass without
