@@ -3,9 +3,10 @@
 //   out[m, n] = act(x_scale[m] * w_scale[n] * sum_k dec(XQ[m,k]) * dec(WQ[n,k]) + bias[n]) + residual[m, n]
 //
 // on the plain GEMM's tiles and launch rules (gemm_kernels.h), with float32
-// values up to the one rounding of the output. Large shapes are bound by the K loop:
-// 4096 x 4096 x 4096 takes 56 to 60 us (2.3 to 2.4 PFLOP/s), with or without
-// activation and residual.
+// values up to the one rounding of the output. Large shapes are bound by the K loop: on
+// one card, replayed from graphs, 4096 x 4096 x 4096 takes 52.3 us in the plain form,
+// 55.5 here without activation and residual (the same bits as the epilogue form), 58.7
+// with the residual and 61.8 (2.2 PFLOP/s) with tanh-GELU and residual.
 #include "gemm_kernels.h"
 
 namespace hq {
@@ -14,7 +15,8 @@ namespace hq {
 // 17 to 64 rows: one barrier
 // ---------------------------------------------------------------------------
 // A decode batch of more than one 16-row block is bound by latency: the weight is
-// read once (14.7 MB at N = 7168, K = 2048: 2.9 us), but a wavefront that walks
+// read once (14.7 MB at N = 7168, K = 2048: 2.4 us at 6.15 TB/s; 33 rows take 6.1 to
+// 6.7, one row in the weight-streaming kernel 4.3 to 4.8), but a wavefront that walks
 // over several chunks of K pays a round trip for each, and adding every slice's
 // sums across wavefronts one after the other costs two barriers a slice. Here a
 // workgroup owns F weight fragments (16 F columns) and all rows, its W wavefronts

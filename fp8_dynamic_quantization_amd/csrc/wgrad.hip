@@ -136,12 +136,15 @@ __global__ __launch_bounds__(1024) void wgrad_colmax_kernel(WgradArgs a, int row
   if (col < a.n) out[(size_t)blockIdx.y * a.n + col] = v;
 }
 
-// Bound by issue and by the matrix cores: at 4096^3 bf16 120 us (1.15 PFLOP/s; a large
-// bf16 library product reaches 1.33), at 2048 x 4096 x 1024 22.6 us (0.76 PFLOP/s; the
-// library's product of the decoded operands 28.0), at 8192 x 4096 x 4096 float32 450 to
-// 483 us on two cards, two products per term. Counters at 2048 x 4096 x 1024: matrix cores busy 29 %, no LDS
-// bank conflicts, 42 % of the issue slots vector instructions, most of them the scaling
-// of G; with the operands in the caches the time is the same.
+// Large shapes are bound by the matrix cores: 4096^3 bf16 118 to 124 us (1.11 to 1.16
+// PFLOP/s; a large bf16 library product reaches 1.33), 8192 x 4096 x 4096 float32 446 to
+// 496 us over several cards, two products per term. 2048 x 4096 x 1024 bf16, one
+// 128 x 128 tile per CU, takes 22.6 to 26 us (0.66 to 0.76 PFLOP/s; the library's product
+// of the decoded operands 28.0): 7 us that do not depend on the tokens and 9.0 to 9.5 per
+// 1024 tokens. Counters there: matrix cores busy 29 %, vector instructions in 42 % of
+// the issue slots (most of them the scaling of G), no LDS bank conflicts, and the same
+// time with the operands in the caches: no unit is saturated, and what a step waits for
+// is not known.
 //
 // Steps [step0, step1) of MS tokens; `part` selects the partial-sum slab when the
 // tokens are split over workgroups.

@@ -492,7 +492,8 @@ hq_status hq_grouped_gemm_a8w8_strict(const uint8_t* xq, int xf, const uint8_t* 
 /* ---------------------------------------------------------------------------
  * Operators around the GEMM of a transformer's linear layers. Their tensors are
  * row-major and contiguous, 16-byte aligned, of one element type `xt` (HQ_F32 or
- * HQ_BF16); all arithmetic is float32 with one rounding per output element.
+ * HQ_BF16); all arithmetic is float32 with one rounding per output element, but for
+ * the terms of a bf16 weight gradient with a scale per token (hq_wgrad_a8).
  * -------------------------------------------------------------------------- */
 
 /* Activations. HQ_ACT_GELU is x * Phi(x) (the erf form), HQ_ACT_GELU_TANH its
@@ -591,8 +592,10 @@ typedef struct hq_fused_epilogue {
  *   out[m, n] = bf16_rne(v), or with out_scale the FP8 code as in
  *               hq_gemm_a8w8_epilogue
  * `ep` is a host pointer and must not be NULL. A bf16 `out` may be the
- * residual's own buffer. Only m <= 16 uses a workspace. All other arguments, the workspace rule and the
- * requirements are those of hq_gemm_a8w8_epilogue. */
+ * residual's own buffer. Only m <= 16 uses a workspace. Without an activation and a
+ * residual the bits are those of hq_gemm_a8w8_epilogue, which is faster above 64
+ * rows. All other arguments, the workspace rule and the requirements are those of
+ * hq_gemm_a8w8_epilogue. */
 hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
                              int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
                              int64_t k, const hq_fused_epilogue* ep, void* out, void* workspace, size_t workspace_bytes,
