@@ -593,8 +593,8 @@ typedef struct hq_fused_epilogue {
  *               hq_gemm_a8w8_epilogue
  * `ep` is a host pointer and must not be NULL. A bf16 `out` may be the
  * residual's own buffer. Only m <= 16 uses a workspace. Without an activation and a
- * residual the bits are those of hq_gemm_a8w8_epilogue, which is faster above 64
- * rows. All other arguments, the workspace rule and the requirements are those of
+ * residual the bits are those of hq_gemm_a8w8_epilogue up to 16 rows and above 64 (where
+ * that one is faster); at 17 to 64 rows the sums are added in another order. All other arguments, the workspace rule and the requirements are those of
  * hq_gemm_a8w8_epilogue. */
 hq_status hq_gemm_a8w8_fused(const uint8_t* xq, int xf, const uint8_t* wq_pre, int wf, const float* x_scale,
                              int64_t x_scale_count, const float* w_scale, int64_t w_scale_count, int64_t m, int64_t n,
