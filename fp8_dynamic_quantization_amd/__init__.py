@@ -7,8 +7,9 @@ from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_A
                    HQ_ERR_UNSUPPORTED_DEVICE, HQ_F32, HQ_OK, HQ_PER_CHANNEL, HQ_PER_TENSOR,
                    HQ_PER_TOKEN, HQError, HQInvalidArgument, HQLaunchError,
                    HQUnsupportedDevice, LIB_PATH, SIGNATURES, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_ring, load)
-from .api import (Checkpoint, RmsNormQuantized, Ring, hq_act_backward, hq_act_backward_workspace_bytes, hq_act_quantize_fp8,
-                  hq_gemm_a8w8_fused, hq_rmsnorm_backward, hq_rmsnorm_backward_workspace_bytes, hq_rmsnorm_quantize_fp8,
+from .api import (Checkpoint, LayerNormQuantized, RmsNormQuantized, Ring, hq_act_backward, hq_act_backward_workspace_bytes, hq_act_quantize_fp8,
+                  hq_gemm_a8w8_fused, hq_layernorm_backward, hq_layernorm_backward_workspace_bytes, hq_layernorm_quantize_fp8,
+                  hq_rmsnorm_backward, hq_rmsnorm_backward_workspace_bytes, hq_rmsnorm_quantize_fp8,
                   hq_wgrad_a8, hq_wgrad_a8_strict, hq_wgrad_workspace_bytes, gemm_workspace, hq_gemm_a8w8, hq_gemm_a8w8_blockscaled, hq_gemm_a8w8_epilogue,
                   hq_gemm_a8w8_blockscaled_preshuffled,
                   hq_gemm_workspace_bytes, hq_quantize_fp8_blockwise, hq_grouped_gemm_a8w8,
@@ -35,4 +36,5 @@ __all__ = [
     "hq_checkpoint", "hq_fused_epilogue", "hq_rmsnorm_quantize_fp8", "hq_rmsnorm_backward",
     "hq_rmsnorm_backward_workspace_bytes", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward",
     "hq_act_backward_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict", "hq_wgrad_workspace_bytes",
+    "LayerNormQuantized", "hq_layernorm_quantize_fp8", "hq_layernorm_backward", "hq_layernorm_backward_workspace_bytes",
 ]

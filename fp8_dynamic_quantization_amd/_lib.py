@@ -117,6 +117,11 @@ SIGNATURES = {
                                      ctypes.POINTER(hq_checkpoint), _P]),
     "hq_rmsnorm_backward_workspace_bytes": (_SZ, [_I, _I64, _I64]),
     "hq_rmsnorm_backward": (_I, [_P, _P, ctypes.POINTER(hq_checkpoint), _P, _P, _P, _I, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "hq_layernorm_quantize_fp8": (_I, [_P, _P, _P, _P, _I, _I64, _I64, ctypes.c_float, _I, _P, _P, _P, _P, _P,
+                                       ctypes.POINTER(hq_checkpoint), _P]),
+    "hq_layernorm_backward_workspace_bytes": (_SZ, [_I, _I64, _I64]),
+    "hq_layernorm_backward": (_I, [_P, _P, ctypes.POINTER(hq_checkpoint), _P, _P, _P, _P, _I, _I64, _I64, _P, _P, _P, _P, _SZ,
+                                   _P]),
     "hq_gemm_a8w8_fused": (_I, [_P, _I, _P, _I, _P, _I64, _P, _I64, _I64, _I64, _I64, ctypes.POINTER(hq_fused_epilogue),
                                 _P, _P, _SZ, _P]),
     "hq_act_quantize_fp8": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _P, _P, ctypes.POINTER(hq_checkpoint), _P]),

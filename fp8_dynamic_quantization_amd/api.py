@@ -33,6 +33,7 @@ __all__ = [
     "Checkpoint", "RmsNormQuantized", "hq_rmsnorm_quantize_fp8", "hq_rmsnorm_backward_workspace_bytes",
     "hq_rmsnorm_backward", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward_workspace_bytes",
     "hq_act_backward", "hq_wgrad_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict",
+    "LayerNormQuantized", "hq_layernorm_quantize_fp8", "hq_layernorm_backward_workspace_bytes", "hq_layernorm_backward",
 ]
 
 _XT = {torch.float32: HQ_F32, torch.bfloat16: HQ_BF16}
@@ -646,6 +647,53 @@ def hq_rmsnorm_backward(dy: torch.Tensor, h, weight: torch.Tensor | None, rstd: 
     want = dweight is not False
     return _native().rmsnorm_backward(dy, h, cq, cs, bs, weight, rstd, dresidual, dx, dweight if want else None, want,
                                       workspace)
+
+
+class LayerNormQuantized(NamedTuple):
+    """Result of hq_layernorm_quantize_fp8; h and checkpoint are None where not asked for."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    h: torch.Tensor | None
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    checkpoint: Checkpoint | None
+
+
+def hq_layernorm_quantize_fp8(x: torch.Tensor, weight: torch.Tensor | None, bias: torch.Tensor | None, eps: float = 1e-5,
+                              fmt: int = HQ_E4M3, *, residual: torch.Tensor | None = None, h=None, checkpoint=None, q=None,
+                              scale_out=None, mean_out=None, rstd_out=None, stream=None) -> LayerNormQuantized:
+    """Layer norm of x (+ residual) [rows, cols] with weight and bias [cols] (None: ones,
+    zeros), quantized per token; `h` and `checkpoint` as in hq_rmsnorm_quantize_fp8."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_layernorm_quantize_fp8(x, weight, bias, eps, fmt, residual=residual, h=h, checkpoint=checkpoint, q=q,
+                                             scale_out=scale_out, mean_out=mean_out, rstd_out=rstd_out)
+    write_h = h is not False and not (h is None and residual is None)
+    cq, cs, bs = _checkpoint_args(checkpoint)
+    q, s, h, m, r, cq, cs = _native().layernorm_quantize(x, weight, bias, eps, fmt, residual, h if write_h else None, write_h,
+                                                         cq, cs, bs, q, scale_out, mean_out, rstd_out)
+    return LayerNormQuantized(q, s, h, m, r, Checkpoint(cq, cs, bs) if bs else None)
+
+
+def hq_layernorm_backward_workspace_bytes(xt: int, rows: int, cols: int) -> int:
+    return int(load().hq_layernorm_backward_workspace_bytes(xt, rows, cols))
+
+
+def hq_layernorm_backward(dy: torch.Tensor, h, weight: torch.Tensor | None, mean: torch.Tensor, rstd: torch.Tensor, *,
+                          dresidual: torch.Tensor | None = None, dx=None, dweight=None, dbias=None, workspace=None,
+                          stream=None):
+    """Backward pass of hq_layernorm_quantize_fp8: returns (dx of dy's type, dweight and
+    dbias float32 [cols]). `h` is the normed tensor in dy's type or its Checkpoint;
+    `dresidual` is added to dx, which may be dy or dresidual itself; `dweight` or `dbias`
+    False leaves that sum over rows out (None returned)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_layernorm_backward(dy, h, weight, mean, rstd, dresidual=dresidual, dx=dx, dweight=dweight, dbias=dbias,
+                                         workspace=workspace)
+    cq, cs, bs, h = (*h, None) if isinstance(h, Checkpoint) else (None, None, 0, h)
+    want_w, want_b = dweight is not False, dbias is not False
+    return _native().layernorm_backward(dy, h, cq, cs, bs, weight, mean, rstd, dresidual, dx, dweight if want_w else None,
+                                        want_w, dbias if want_b else None, want_b, workspace)
 
 
 def hq_gemm_a8w8_fused(xq: torch.Tensor, xf: int, wq_pre: torch.Tensor, wf: int, x_scale: torch.Tensor,

@@ -830,9 +830,10 @@ static size_t checkpoint_scale_bytes(const hq_checkpoint* c, int64_t rows, int64
   return (size_t)rows * (size_t)((wide + c->block_size - 1) / c->block_size) * 4;
 }
 
-hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, int xt, int64_t rows,
-                                  int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out, void* h_out,
-                                  float* rstd_out, const hq_checkpoint* ckpt, hipStream_t stream) {
+// The forward norms: `ln` takes the bias and writes the mean.
+static hq_status norm_impl(const void* x, const void* residual, const void* weight, const void* bias, int xt, int64_t rows,
+                           int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out, void* h_out, float* mean_out,
+                           float* rstd_out, const hq_checkpoint* ckpt, bool ln, const char* name, hipStream_t stream) {
   hq_status st = check_rows(xt, rows, cols, cols);
   if (st != HQ_OK) return st;
   if (!valid_fmt(fmt)) return fail(HQ_ERR_INVALID_ARGUMENT, "fmt must be HQ_E4M3 or HQ_E5M2, got %d", fmt);
@@ -843,10 +844,11 @@ hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const voi
   }
   if (rows == 0) return ok();
   if (!x || !q || !scale_out) return fail(HQ_ERR_INVALID_ARGUMENT, "x, q and scale_out must be non-NULL");
-  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(q, 16) || !aligned(h_out, 16))
-    return fail(HQ_ERR_INVALID_ARGUMENT, "x, residual, weight, q and h_out must be 16-byte aligned");
-  if (!aligned(scale_out, 4) || !aligned(rstd_out, 4))
-    return fail(HQ_ERR_INVALID_ARGUMENT, "scale_out and rstd_out must be 4-byte aligned");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(q, 16) ||
+      !aligned(h_out, 16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x, residual, weight, bias, q and h_out must be 16-byte aligned");
+  if (!aligned(scale_out, 4) || !aligned(mean_out, 4) || !aligned(rstd_out, 4))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "scale_out, mean_out and rstd_out must be 4-byte aligned");
   const size_t numel = (size_t)rows * (size_t)cols, es = xt == HQ_BF16 ? 2 : 4;
   // the outputs first; h_out may be x or the residual itself
   const Range rg[] = {
@@ -854,20 +856,38 @@ hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const voi
       {scale_out, (size_t)rows * 4, "scale_out"},
       {h_out, numel * es, "h_out"},
       {rstd_out, (size_t)rows * 4, "rstd_out"},
+      {mean_out, (size_t)rows * 4, "mean_out"},
       {ckpt ? ckpt->q : nullptr, numel, "checkpoint q"},
       {ckpt ? ckpt->scales : nullptr, ckpt ? checkpoint_scale_bytes(ckpt, rows, cols) : 0, "checkpoint scales"},
       {x == h_out ? nullptr : x, numel * es, "x"},
       {residual == h_out ? nullptr : residual, numel * es, "residual"},
       {weight, (size_t)cols * es, "weight"},
+      {bias, (size_t)cols * es, "bias"},
   };
-  st = check_outputs(rg, 9, 6);
+  st = check_outputs(rg, 11, 7);
   if (st != HQ_OK) return st;
   st = check_device();
   if (st != HQ_OK) return st;
   (void)hipGetLastError();
   const hq::NormArgs a{x, residual, weight, h_out, q, scale_out, rstd_out, ckpt ? ckpt->q : nullptr,
-                       ckpt ? ckpt->scales : nullptr, (int)rows, (int)cols, ckpt ? ckpt->block_size : 0, fmt, eps};
-  return launched(hq::launch_rmsnorm_quant(a, xt, stream), "hq_rmsnorm_quantize_fp8");
+                       ckpt ? ckpt->scales : nullptr, (int)rows, (int)cols, ckpt ? ckpt->block_size : 0, fmt, eps, bias,
+                       mean_out};
+  return launched(ln ? hq::launch_layernorm_quant(a, xt, stream) : hq::launch_rmsnorm_quant(a, xt, stream), name);
+}
+
+hq_status hq_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, int xt, int64_t rows,
+                                  int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out, void* h_out,
+                                  float* rstd_out, const hq_checkpoint* ckpt, hipStream_t stream) {
+  return norm_impl(x, residual, weight, nullptr, xt, rows, cols, eps, fmt, q, scale_out, h_out, nullptr, rstd_out, ckpt, false,
+                   "hq_rmsnorm_quantize_fp8", stream);
+}
+
+hq_status hq_layernorm_quantize_fp8(const void* x, const void* residual, const void* weight, const void* bias, int xt,
+                                    int64_t rows, int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out,
+                                    void* h_out, float* mean_out, float* rstd_out, const hq_checkpoint* ckpt,
+                                    hipStream_t stream) {
+  return norm_impl(x, residual, weight, bias, xt, rows, cols, eps, fmt, q, scale_out, h_out, mean_out, rstd_out, ckpt, true,
+                   "hq_layernorm_quantize_fp8", stream);
 }
 
 size_t hq_rmsnorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols) {
@@ -885,9 +905,11 @@ static hq_status check_sum_workspace(const void* workspace, size_t workspace_byt
   return HQ_OK;
 }
 
-hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
-                              const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
-                              float* dweight, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+// Their backward passes: `ln` takes the mean and sums dbias.
+static hq_status norm_bwd_impl(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight, const float* mean,
+                               const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
+                               float* dweight, float* dbias, void* workspace, size_t workspace_bytes, bool ln,
+                               const char* name, hipStream_t stream) {
   hq_status st = check_rows(xt, rows, cols, cols);
   if (st != HQ_OK) return st;
   if (ckpt) {
@@ -896,40 +918,70 @@ hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint
   }
   if (rows > 0 && (h != nullptr) == (ckpt != nullptr)) return fail(HQ_ERR_INVALID_ARGUMENT, "give h or ckpt, not both");
   if (!aligned(dweight, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "dweight must be 16-byte aligned");
-  size_t need = 0;
+  if (!aligned(dbias, 16)) return fail(HQ_ERR_INVALID_ARGUMENT, "dbias must be 16-byte aligned");
+  const bool sums = dweight || dbias;
+  const size_t col_bytes = (size_t)cols * 4;
   if (rows > 0) {
     if (!dy || !rstd || !dx) return fail(HQ_ERR_INVALID_ARGUMENT, "dy, rstd and dx must be non-NULL");
+    if (ln && !mean) return fail(HQ_ERR_INVALID_ARGUMENT, "mean must be non-NULL");
     if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dresidual, 16) || !aligned(dx, 16))
       return fail(HQ_ERR_INVALID_ARGUMENT, "dy, h, weight, dresidual and dx must be 16-byte aligned");
-    if (!aligned(rstd, 4)) return fail(HQ_ERR_INVALID_ARGUMENT, "rstd must be 4-byte aligned");
-    need = dweight ? hq::rmsnorm_bwd_workspace_bytes((int)rows, (int)cols, xt) : 0;
+    if (!aligned(rstd, 4) || !aligned(mean, 4)) return fail(HQ_ERR_INVALID_ARGUMENT, "mean and rstd must be 4-byte aligned");
+    const size_t need = !sums ? 0
+                        : ln  ? hq::layernorm_bwd_workspace_bytes((int)rows, (int)cols, xt)
+                              : hq::rmsnorm_bwd_workspace_bytes((int)rows, (int)cols, xt);
     st = check_sum_workspace(workspace, workspace_bytes, need);
     if (st != HQ_OK) return st;
     const size_t numel = (size_t)rows * (size_t)cols, es = xt == HQ_BF16 ? 2 : 4;
     const Range rg[] = {
         {dx, numel * es, "dx"},
-        {dweight, (size_t)cols * 4, "dweight"},
+        {dweight, col_bytes, "dweight"},
+        {dbias, col_bytes, "dbias"},
         {workspace, need, "workspace"},
         {dy == dx ? nullptr : dy, numel * es, "dy"},
         {h, numel * es, "h"},
         {ckpt ? ckpt->q : nullptr, numel, "checkpoint q"},
         {ckpt ? ckpt->scales : nullptr, ckpt ? checkpoint_scale_bytes(ckpt, rows, cols) : 0, "checkpoint scales"},
         {weight, (size_t)cols * es, "weight"},
+        {mean, (size_t)rows * 4, "mean"},
         {rstd, (size_t)rows * 4, "rstd"},
         {dresidual == dx ? nullptr : dresidual, numel * es, "dresidual"},
     };
-    st = check_outputs(rg, 10, 3);
+    st = check_outputs(rg, 12, 4);
     if (st != HQ_OK) return st;
-  } else if (!dweight) {
-    return ok();
+  } else {
+    if (!sums) return ok();
+    const Range rg[] = {{dweight, col_bytes, "dweight"}, {dbias, col_bytes, "dbias"}};
+    st = check_outputs(rg, 2, 2);
+    if (st != HQ_OK) return st;
   }
   st = check_device();
   if (st != HQ_OK) return st;
   (void)hipGetLastError();
   const hq::NormBwdArgs a{dy, h, ckpt ? ckpt->q : nullptr, ckpt ? ckpt->scales : nullptr, weight, rstd, dresidual, dx,
-                          dweight, dweight ? static_cast<float*>(workspace) : nullptr, (int)rows, (int)cols,
-                          ckpt ? ckpt->block_size : 0};
-  return launched(hq::launch_rmsnorm_bwd(a, xt, stream), "hq_rmsnorm_backward");
+                          dweight, sums ? static_cast<float*>(workspace) : nullptr, (int)rows, (int)cols,
+                          ckpt ? ckpt->block_size : 0, mean, dbias};
+  return launched(ln ? hq::launch_layernorm_bwd(a, xt, stream) : hq::launch_rmsnorm_bwd(a, xt, stream), name);
+}
+
+hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
+                              const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
+                              float* dweight, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return norm_bwd_impl(dy, h, ckpt, weight, nullptr, rstd, dresidual, xt, rows, cols, dx, dweight, nullptr, workspace,
+                       workspace_bytes, false, "hq_rmsnorm_backward", stream);
+}
+
+size_t hq_layernorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols) {
+  if (!row_sizes(xt, rows, cols, cols) || rows == 0) return 0;
+  return hq::layernorm_bwd_workspace_bytes((int)rows, (int)cols, xt);
+}
+
+hq_status hq_layernorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
+                                const float* mean, const float* rstd, const void* dresidual, int xt, int64_t rows,
+                                int64_t cols, void* dx, float* dweight, float* dbias, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  return norm_bwd_impl(dy, h, ckpt, weight, mean, rstd, dresidual, xt, rows, cols, dx, dweight, dbias, workspace,
+                       workspace_bytes, true, "hq_layernorm_backward", stream);
 }
 
 static hq_status check_act(int act, int gated) {

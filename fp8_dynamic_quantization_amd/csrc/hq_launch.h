@@ -164,8 +164,9 @@ hipError_t launch_grouped_gemm(const GemmArgs& a, const int32_t* offsets, int ex
 // Sums of `parts` partial rows [parts, cols] in order; parts == 0 gives zeros.
 hipError_t launch_column_sums(const float* partials, int parts, int cols, float* out, hipStream_t st);
 
-// RMS norm with residual and FP8 output. Null pointers leave out what they
-// name; cblock is 0 without a checkpoint, else 32, 64 or 128.
+// RMS norm or layer norm with residual and FP8 output. Null pointers leave out what
+// they name; cblock is 0 without a checkpoint, else 32, 64 or 128. bias and mean
+// are the layer norm's.
 struct NormArgs {
   const void* x;         // [rows, cols]
   const void* residual;  // [rows, cols] or null
@@ -178,8 +179,11 @@ struct NormArgs {
   float* cs;             // checkpoint scales [rows, ceil(cols / cblock)]
   int rows, cols, cblock, fmt;
   float eps;
+  const void* bias;      // [cols] or null (zeros)
+  float* mean;           // [rows] or null
 };
 hipError_t launch_rmsnorm_quant(const NormArgs& a, int xt, hipStream_t st);
+hipError_t launch_layernorm_quant(const NormArgs& a, int xt, hipStream_t st);
 
 struct NormBwdArgs {
   const void* dy;      // [rows, cols]
@@ -191,11 +195,15 @@ struct NormBwdArgs {
   const void* dres;    // [rows, cols] or null
   void* dx;            // [rows, cols]
   float* dw;           // [cols] or null
-  float* partials;     // workspace, null exactly when dw is
+  float* partials;     // workspace, null exactly when dw and db are
   int rows, cols, cblock;
+  const float* mean;   // layer norm: [rows]
+  float* db;           // layer norm: [cols] or null
 };
 size_t rmsnorm_bwd_workspace_bytes(int rows, int cols, int xt);
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st);
+size_t layernorm_bwd_workspace_bytes(int rows, int cols, int xt);
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st);
 
 // Activation into FP8 codes; z is [rows, cols], gated [rows, 2 cols].
 struct ActArgs {

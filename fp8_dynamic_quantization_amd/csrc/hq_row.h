@@ -108,6 +108,28 @@ __device__ __forceinline__ float row_sum_f32(float v, float* slot, int wave) {
   for (int i = 1; i < WPR; ++i) t += slot[i];
   return t;
 }
+// Two totals in one exchange.
+template <int WPR>
+__device__ __forceinline__ void row_sum2_f32(float v, float u, float* slot, float* slot2, int wave, float* vs, float* us) {
+  v = wave_sum_f32(v);
+  u = wave_sum_f32(u);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      slot[wave] = v;
+      slot2[wave] = u;
+    }
+    __syncthreads();
+    v = slot[0];
+    u = slot2[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) {
+      v += slot[i];
+      u += slot2[i];
+    }
+  }
+  *vs = v;
+  *us = u;
+}
 template <int WPR>
 __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, uint32_t* slot, int wave) {
   v = wave_max_u32(v);

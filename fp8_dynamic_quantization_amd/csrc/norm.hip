@@ -1,11 +1,18 @@
-// RMS norm with the residual's addition and FP8 output, and its backward pass,
-// gfx950.
+// RMS norm and layer norm with the residual's addition and FP8 output, and their
+// backward passes, gfx950.
 //
 //   forward   h = x + residual            rstd = 1 / sqrt(mean_c h^2 + eps)
 //             y = (h * rstd) * w          s = max(amax_row(y) / fmax, 2^-126)
 //             q = cast(y * (1 / s))       optionally h itself and an 8-bit block-wise checkpoint of it
 //   backward  xh = h * rstd, t = dy * w   dx = dres + rstd * (t - xh * mean_c(t * xh))
 //             dw = sum_rows dy * xh
+//
+// Layer norm (LN) has d = h - mean_c h in h's place, and a bias:
+//   forward   rstd = 1 / sqrt(mean_c d^2 + eps), y = (d * rstd) * w + b
+//   backward  xh = d * rstd, dx = dres + rstd * (t - mean_c t - xh * mean_c(t * xh)), db = sum_rows dy
+// Its sum of squares is taken of the differences, which the registers hold by then
+// (one more exchange across a row's wavefronts): sums of h and h^2 in one go cancel
+// where a row's mean is large beside its deviation.
 //
 // All sums are float32; h enters the statistics and y unrounded.
 #include "hq_launch.h"
@@ -27,12 +34,12 @@ struct NormFwd {
   static constexpr int kThreads = kRowThreads * kRows;
 };
 
-template <int XT, int WPR, int NV>
-__global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void rmsnorm_quant_kernel(NormArgs a) {
+template <bool LN, int XT, int WPR, int NV>
+__global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_kernel(NormArgs a) {
   using C = NormFwd<XT, WPR, NV>;
   constexpr int E = C::E;
   static_assert(WPR == 1 || C::kRows == 1, "one row per workgroup where a row needs its barrier");
-  __shared__ float s_sum[WPR];
+  __shared__ float s_sum[WPR], s_mean[LN ? WPR : 1];
   __shared__ uint32_t s_max[WPR], s_fin[WPR];
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % WPR);
   const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / C::kRowThreads);
@@ -47,6 +54,12 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void rmsnorm_quan
   const __amdgpu_buffer_rsrc_t w_rsrc = row_rsrc(a.weight, a.weight ? row_bytes : 0u);
 #pragma unroll
   for (int j = 0; j < NV; ++j) w[j] = row_load16(w_rsrc, off0 + j * 16 * C::kRowThreads);
+  uint4 b[LN ? NV : 1];
+  if constexpr (LN) {
+    const __amdgpu_buffer_rsrc_t b_rsrc = row_rsrc(a.bias, a.bias ? row_bytes : 0u);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) b[j] = row_load16(b_rsrc, off0 + j * 16 * C::kRowThreads);
+  }
 
   const int64_t step = (int64_t)gridDim.x * C::kRows;
   for (int64_t row = (int64_t)blockIdx.x * C::kRows + grp; row < a.rows; row += step) {
@@ -76,7 +89,7 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void rmsnorm_quan
     for (int j = 0; j < NV; ++j) {
       ss[j] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss[j] = fmaf(v[j][e], v[j][e], ss[j]);
+      for (int e = 0; e < E; ++e) ss[j] = LN ? ss[j] + v[j][e] : fmaf(v[j][e], v[j][e], ss[j]);
     }
 #pragma unroll
     for (int j = 1; j < NV; ++j) ss[0] += ss[j];
@@ -99,13 +112,32 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void rmsnorm_quan
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), cs_rsrc, i / g * 4, 0, 0);
       }
     }
+    float mean = 0.0f;
+    if constexpr (LN) {
+      mean = row_sum_f32<WPR>(ss[0], s_mean, wave) / (float)a.cols;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const bool in = (t + j * C::kRowThreads) * E < a.cols;  // past the row's end the difference stays 0
+        ss[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          v[j][e] = in ? v[j][e] - mean : 0.0f;
+          ss[j] = fmaf(v[j][e], v[j][e], ss[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 1; j < NV; ++j) ss[0] += ss[j];
+    }
     const float total = row_sum_f32<WPR>(ss[0], s_sum, wave);
     const float rstd = 1.0f / sqrtf(fmaf(total, inv_n, a.eps));
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[j][e] = a.weight ? v[j][e] * rstd * vec_elem<XT>(w[j], e) : v[j][e] * rstd;
+      for (int e = 0; e < E; ++e) {
+        v[j][e] = a.weight ? v[j][e] * rstd * vec_elem<XT>(w[j], e) : v[j][e] * rstd;
+        if constexpr (LN) v[j][e] += vec_elem<XT>(b[j], e);
+      }
       m = max(m, absmax_raw<E>(v[j]));
     }
     m = row_max_u32<WPR>(m, s_max, wave);
@@ -130,18 +162,20 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void rmsnorm_quan
     if (t == 0) {
       a.scale[row] = s;
       if (a.rstd) a.rstd[row] = rstd;
+      if (LN && a.mean) a.mean[row] = mean;
     }
   }
 }
 
 // Rows longer than the register form holds: one workgroup of 16 wavefronts per
 // row reads the row three times (sum of squares and checkpoint, maximum, cast
-// and h). h is written in the last pass only, each vector after its own reads,
+// and h), for a layer norm four times (sum and checkpoint, sum of squares of the
+// differences, ...). h is written in the last pass only, each vector after its own reads,
 // so h may be the residual's or x's own buffer here too.
-template <int XT>
-__global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
+template <bool LN, int XT>
+__global__ __launch_bounds__(1024) void norm_quant_long_kernel(NormArgs a) {
   constexpr int E = VecTraits<XT>::kElems;
-  __shared__ float s_sum[16];
+  __shared__ float s_sum[16], s_mean[16];
   __shared__ uint32_t s_max[16], s_fin[16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = threadIdx.x;
@@ -150,6 +184,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
   const int g = a.cblock / E;
   const float inv_n = 1.0f / (float)a.cols;
   const uint4* wv = static_cast<const uint4*>(a.weight);
+  const uint4* bv = LN ? static_cast<const uint4*>(a.bias) : nullptr;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const uint4* x = static_cast<const uint4*>(a.x) + (size_t)row * nvec;
     const uint4* res = a.residual ? static_cast<const uint4*>(a.residual) + (size_t)row * nvec : nullptr;
@@ -170,7 +205,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
       if (i < nvec) load_h(i, v);
       float p = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) p = fmaf(v[e], v[e], p);
+      for (int e = 0; e < E; ++e) p = LN ? p + v[e] : fmaf(v[e], v[e], p);
       ss += p;
       if (a.cblock) {
         uint32_t cw[E / 4];
@@ -181,13 +216,30 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
         }
       }
     }
+    float mean = 0.0f;
+    if constexpr (LN) {
+      mean = row_sum_f32<16>(ss, s_mean, wave) / (float)a.cols;
+      ss = 0.0f;
+      for (int i = t; i < nvec; i += 1024) {
+        float v[E], p = 0.0f;
+        load_h(i, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) p = fmaf(v[e] - mean, v[e] - mean, p);
+        ss += p;
+      }
+    }
     const float total = row_sum_f32<16>(ss, s_sum, wave);
     const float rstd = 1.0f / sqrtf(fmaf(total, inv_n, a.eps));
     auto load_y = [&](int i, float* h, float* y) {
       load_h(i, h);
       const uint4 w = wv ? wv[i] : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 b = LN && bv ? bv[i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = wv ? h[e] * rstd * vec_elem<XT>(w, e) : h[e] * rstd;
+      for (int e = 0; e < E; ++e) {
+        const float d = LN ? h[e] - mean : h[e];
+        y[e] = wv ? d * rstd * vec_elem<XT>(w, e) : d * rstd;
+        if constexpr (LN) y[e] += vec_elem<XT>(b, e);
+      }
     };
     uint32_t raw = 0, fin = 0;
     for (int i = t; i < nvec; i += 1024) {
@@ -212,6 +264,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long_kernel(NormArgs a) {
     if (t == 0) {
       a.scale[row] = s;
       if (a.rstd) a.rstd[row] = rstd;
+      if (LN && a.mean) a.mean[row] = mean;
     }
   }
 }
@@ -236,16 +289,17 @@ constexpr int kBwdLdsFloats = 16384;
 // gets workgroups of its own for it, past the `row_blocks` that compute dx. They
 // read dy and h again, from the caches, and no second launch adds partial sums.
 // (Where dx is dy's own buffer, they go first, in a launch of their own.)
-template <int XT, bool CKPT>
-__device__ __forceinline__ void rmsnorm_dw_columns(const NormBwdArgs& a, int tile, float* s) {
+template <bool LN, int XT, bool CKPT>
+__device__ __forceinline__ void norm_dw_columns(const NormBwdArgs& a, int tile, float* s) {
   constexpr int E = VecTraits<XT>::kElems;
   const int i = tile * kColVecs + (threadIdx.x & 7);  // vector column
   const int nvec = a.cols / E;
   const int nb = CKPT ? (a.cols + a.cblock - 1) / a.cblock : 0;
   const int gsh = CKPT ? __builtin_ctz(a.cblock / E) : 0;
-  float dw[E];
+  constexpr int N = LN ? 2 * E : E;  // dw's sums, then db's
+  float dw[N];
 #pragma unroll
-  for (int e = 0; e < E; ++e) dw[e] = 0.0f;
+  for (int e = 0; e < N; ++e) dw[e] = 0.0f;
   if (i < nvec) {
 #pragma unroll 4
     for (int row = threadIdx.x >> 3; row < a.rows; row += kColSlots) {
@@ -261,27 +315,34 @@ __device__ __forceinline__ void rmsnorm_dw_columns(const NormBwdArgs& a, int til
         vec_widen<XT>(static_cast<const uint4*>(a.h)[(size_t)row * nvec + i], xh);
       }
       const float rstd = a.rstd[row];
+      const float mean = LN ? a.mean[row] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) dw[e] = fmaf(vec_elem<XT>(dy, e), xh[e] * rstd, dw[e]);
+      for (int e = 0; e < E; ++e) {
+        dw[e] = fmaf(vec_elem<XT>(dy, e), (LN ? xh[e] - mean : xh[e]) * rstd, dw[e]);
+        if constexpr (LN) dw[E + e] += vec_elem<XT>(dy, e);
+      }
     }
   }
-  if (slots_sum<E>(dw, s) && i < nvec) {
+  if (!slots_sum<N>(dw, s) || i >= nvec) return;
 #pragma unroll
-    for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(a.dw + (size_t)i * E + e) = make_float4(dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
+  for (int e = 0; e < N; e += 4) {
+    float* out = e < E ? a.dw : a.db;
+    if (out) *reinterpret_cast<float4*>(out + (size_t)i * E + e % E) = make_float4(dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
   }
 }
 
-template <int XT, int WPR, int NV, bool CKPT>
-__global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int row_blocks) {
+template <bool LN, int XT, int WPR, int NV, bool CKPT>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a, int row_blocks) {
   constexpr int E = VecTraits<XT>::kElems;
   constexpr int kRowThreads = 64 * WPR;
   constexpr int kGroups = 16 / WPR;
   constexpr int kCols = kRowThreads * NV * E;
   static_assert(kGroups == 1 || kCols * (kGroups / 2) <= kBwdLdsFloats, "row groups meet in LDS");
   constexpr int kPart = kGroups > 1 ? kCols * (kGroups / 2) : 1;
-  __shared__ float s_part[kPart < 16 * 8 * E ? 16 * 8 * E : kPart];
-  __shared__ float s_sum[2][16];
-  if ((int)blockIdx.x >= row_blocks) return rmsnorm_dw_columns<XT, CKPT>(a, blockIdx.x - row_blocks, s_part);
+  constexpr int kSlots = 16 * 8 * (LN ? 2 * E : E);  // of norm_dw_columns
+  __shared__ float s_part[kPart < kSlots ? kSlots : kPart];
+  __shared__ float s_sum[2][16], s_mean[2][LN ? 16 : 1];
+  if ((int)blockIdx.x >= row_blocks) return norm_dw_columns<LN, XT, CKPT>(a, blockIdx.x - row_blocks, s_part);
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % WPR);
   const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / kRowThreads);
   const int t = threadIdx.x % kRowThreads;
@@ -295,11 +356,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int ro
   const __amdgpu_buffer_rsrc_t w_rsrc = row_rsrc(a.weight, a.weight ? row_bytes : 0u);
 #pragma unroll
   for (int j = 0; j < NV; ++j) w[j] = row_load16(w_rsrc, off0 + j * 16 * kRowThreads);
-  float dw[NV][E];
+  float dw[NV][E], db[LN ? NV : 1][E];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < E; ++e) dw[j][e] = 0.0f;
+    for (int e = 0; e < E; ++e) {
+      dw[j][e] = 0.0f;
+      if constexpr (LN) db[j][e] = 0.0f;
+    }
 
   int parity = 0;
   // the trip count is uniform over the workgroup; groups past the last row read
@@ -333,25 +397,38 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int ro
 #pragma unroll
     for (int j = 0; j < NV; ++j) rv[j] = row_load16(r_rsrc, off0 + j * 16 * kRowThreads);
     const float rstd = live ? a.rstd[row] : 0.0f;
+    const float mean = LN && live ? a.mean[row] : 0.0f;
 
     float xh[NV][E];
-    float dot = 0.0f;
+    float dot = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if constexpr (CKPT) decode_vec<E>(hc[j], hs[j], xh[j]);
       else vec_widen<XT>(hv[j], xh[j]);
-      float p = 0.0f;
+      float p = 0.0f, q = 0.0f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        xh[j][e] *= rstd;
+        xh[j][e] = LN ? (xh[j][e] - mean) * rstd : xh[j][e] * rstd;
         const float d = vec_elem<XT>(dy[j], e);
         const float tt = a.weight ? d * vec_elem<XT>(w[j], e) : d;
         p = fmaf(tt, xh[j][e], p);
         dw[j][e] = fmaf(d, xh[j][e], dw[j][e]);
+        if constexpr (LN) {
+          q += tt;
+          db[j][e] += d;
+        }
       }
       dot += p;
+      if constexpr (LN) sum += q;
     }
-    const float c = row_sum_f32<WPR>(dot, s_sum[parity] + grp * WPR, wave) * inv_n;
+    float c, c0 = 0.0f;
+    if constexpr (LN) {
+      row_sum2_f32<WPR>(dot, sum, s_sum[parity] + grp * WPR, s_mean[parity] + grp * WPR, wave, &c, &c0);
+      c *= inv_n;
+      c0 *= inv_n;
+    } else {
+      c = row_sum_f32<WPR>(dot, s_sum[parity] + grp * WPR, wave) * inv_n;
+    }
     parity ^= 1;
     const __amdgpu_buffer_rsrc_t o_rsrc = row_rsrc(static_cast<uint8_t*>(a.dx) + at, bytes);
 #pragma unroll
@@ -361,7 +438,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int ro
       for (int e = 0; e < E; ++e) {
         const float d = vec_elem<XT>(dy[j], e);
         const float tt = a.weight ? d * vec_elem<XT>(w[j], e) : d;
-        const float n = fmaf(-xh[j][e], c, tt) * rstd;
+        const float n = fmaf(-xh[j][e], c, LN ? tt - c0 : tt) * rstd;
         o[e] = a.dres ? n + vec_elem<XT>(rv[j], e) : n;
       }
       row_store16<0>(o_rsrc, off0 + j * 16 * kRowThreads, vec_narrow<XT>(o));
@@ -369,37 +446,43 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, int ro
   }
   if (!a.partials) return;
 
-  // Row groups, upper half onto lower half until one is left.
+  // Row groups, upper half onto lower half until one is left; `part` is the
+  // workgroup's partial row of these sums.
+  auto write_sums = [&](float (&sums)[NV][E], float* part) {
 #pragma unroll
-  for (int half = kGroups / 2; half >= 1; half /= 2) {
-    __syncthreads();
-    if (grp >= half && grp < 2 * half) {
+    for (int half = kGroups / 2; half >= 1; half /= 2) {
+      __syncthreads();
+      if (grp >= half && grp < 2 * half) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_part[((grp - half) * NV * E + j * E + e) * kRowThreads + t] = dw[j][e];
+          for (int e = 0; e < E; ++e) s_part[((grp - half) * NV * E + j * E + e) * kRowThreads + t] = sums[j][e];
+      }
+      __syncthreads();
+      if (grp < half) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < E; ++e) sums[j][e] += s_part[(grp * NV * E + j * E + e) * kRowThreads + t];
+      }
     }
-    __syncthreads();
-    if (grp < half) {
+    if (grp != 0) return;
+    const __amdgpu_buffer_rsrc_t p_rsrc = row_rsrc(part, (uint32_t)a.cols * 4u);
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) dw[j][e] += s_part[(grp * NV * E + j * E + e) * kRowThreads + t];
-    }
-  }
-  if (grp != 0) return;
-  const __amdgpu_buffer_rsrc_t p_rsrc = row_rsrc(a.partials + (size_t)blockIdx.x * a.cols, (uint32_t)a.cols * 4u);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < E; e += 4)
-      row_store16<0>(p_rsrc, ((t + j * kRowThreads) * E + e) * 4, vec_narrow<kF32>(dw[j] + e));
+      for (int e = 0; e < E; e += 4)
+        row_store16<0>(p_rsrc, ((t + j * kRowThreads) * E + e) * 4, vec_narrow<kF32>(sums[j] + e));
+  };
+  float* part = a.partials + (size_t)blockIdx.x * a.cols * (LN ? 2 : 1);
+  write_sums(dw, part);
+  if constexpr (LN) write_sums(db, part + a.cols);
 }
 
 // Rows longer than the register form holds: dx by one workgroup of 16
 // wavefronts per row, which reads the row twice, and the rows' partial dw by
 // column tiles of 1024 vectors.
-template <int XT, bool CKPT>
+template <bool LN, int XT, bool CKPT>
 struct LongRow {
   static constexpr int E = VecTraits<XT>::kElems;
   const NormBwdArgs& a;
@@ -415,32 +498,45 @@ struct LongRow {
     } else {
       vec_widen<XT>(static_cast<const uint4*>(a.h)[(size_t)row * nvec + i], xh);
     }
+    const float mean = LN ? a.mean[row] : 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) xh[e] *= rstd;
+    for (int e = 0; e < E; ++e) xh[e] = LN ? (xh[e] - mean) * rstd : xh[e] * rstd;
   }
 };
 
-template <int XT, bool CKPT>
-__global__ __launch_bounds__(1024) void rmsnorm_bwd_dx_long_kernel(NormBwdArgs a) {
+template <bool LN, int XT, bool CKPT>
+__global__ __launch_bounds__(1024) void norm_bwd_dx_long_kernel(NormBwdArgs a) {
   constexpr int E = VecTraits<XT>::kElems;
-  __shared__ float s_sum[2][16];
+  __shared__ float s_sum[2][16], s_mean[2][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const LongRow<XT, CKPT> lr{a, a.cols / E, CKPT ? (a.cols + a.cblock - 1) / a.cblock : 0};
+  const LongRow<LN, XT, CKPT> lr{a, a.cols / E, CKPT ? (a.cols + a.cblock - 1) / a.cblock : 0};
   const uint4* wv = static_cast<const uint4*>(a.weight);
   const float inv_n = 1.0f / (float)a.cols;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float rstd = a.rstd[row];
-    float dot = 0.0f;
+    float dot = 0.0f, sum = 0.0f;
     for (int i = threadIdx.x; i < lr.nvec; i += 1024) {
-      float dy[E], xh[E], p = 0.0f;
+      float dy[E], xh[E], p = 0.0f, q = 0.0f;
       lr.load(row, i, rstd, dy, xh);
       const uint4 w = wv ? wv[i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int e = 0; e < E; ++e) p = fmaf(wv ? dy[e] * vec_elem<XT>(w, e) : dy[e], xh[e], p);
+      for (int e = 0; e < E; ++e) {
+        const float tt = wv ? dy[e] * vec_elem<XT>(w, e) : dy[e];
+        p = fmaf(tt, xh[e], p);
+        if constexpr (LN) q += tt;
+      }
       dot += p;
+      if constexpr (LN) sum += q;
     }
-    const float c = row_sum_f32<16>(dot, s_sum[parity], wave) * inv_n;
+    float c, c0 = 0.0f;
+    if constexpr (LN) {
+      row_sum2_f32<16>(dot, sum, s_sum[parity], s_mean[parity], wave, &c, &c0);
+      c *= inv_n;
+      c0 *= inv_n;
+    } else {
+      c = row_sum_f32<16>(dot, s_sum[parity], wave) * inv_n;
+    }
     parity ^= 1;
     for (int i = threadIdx.x; i < lr.nvec; i += 1024) {
       float dy[E], xh[E], o[E];
@@ -449,7 +545,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dx_long_kernel(NormBwdArgs a
       const uint4 rv = a.dres ? static_cast<const uint4*>(a.dres)[(size_t)row * lr.nvec + i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float n = fmaf(-xh[e], c, wv ? dy[e] * vec_elem<XT>(w, e) : dy[e]) * rstd;
+        const float tt = wv ? dy[e] * vec_elem<XT>(w, e) : dy[e];
+        const float n = fmaf(-xh[e], c, LN ? tt - c0 : tt) * rstd;
         o[e] = a.dres ? n + vec_elem<XT>(rv, e) : n;
       }
       static_cast<uint4*>(a.dx)[(size_t)row * lr.nvec + i] = vec_narrow<XT>(o);
@@ -457,24 +554,30 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dx_long_kernel(NormBwdArgs a
   }
 }
 
-template <int XT, bool CKPT>
-__global__ __launch_bounds__(1024) void rmsnorm_bwd_dw_long_kernel(NormBwdArgs a) {
+template <bool LN, int XT, bool CKPT>
+__global__ __launch_bounds__(1024) void norm_bwd_dw_long_kernel(NormBwdArgs a) {
   constexpr int E = VecTraits<XT>::kElems;
-  const LongRow<XT, CKPT> lr{a, a.cols / E, CKPT ? (a.cols + a.cblock - 1) / a.cblock : 0};
+  const LongRow<LN, XT, CKPT> lr{a, a.cols / E, CKPT ? (a.cols + a.cblock - 1) / a.cblock : 0};
   const int i = blockIdx.x * 1024 + threadIdx.x;
   if (i >= lr.nvec) return;
-  float dw[E];
+  float dw[E], db[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) dw[e] = 0.0f;
+  for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.0f;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     float dy[E], xh[E];
     lr.load(row, i, a.rstd[row], dy, xh);
 #pragma unroll
-    for (int e = 0; e < E; ++e) dw[e] = fmaf(dy[e], xh[e], dw[e]);
+    for (int e = 0; e < E; ++e) {
+      dw[e] = fmaf(dy[e], xh[e], dw[e]);
+      if constexpr (LN) db[e] += dy[e];
+    }
   }
-  float* p = a.partials + (size_t)blockIdx.y * a.cols + (size_t)i * E;
+  float* p = a.partials + (size_t)blockIdx.y * a.cols * (LN ? 2 : 1) + (size_t)i * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) p[e] = dw[e];
+  for (int e = 0; e < E; ++e) {
+    p[e] = dw[e];
+    if constexpr (LN) p[(size_t)a.cols + e] = db[e];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -483,9 +586,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_dw_long_kernel(NormBwdArgs a
 // out[c] = sum_p partials[p][c]: 64 columns per workgroup, wavefront w takes
 // the partial rows w, w + 16, ..., and the 16 sums are added in order. With no
 // partial rows the sums are zero. 2.4 us for 256 x 4096 (the partials come from the
-// caches they were just written to).
-__global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ partials, int parts, int cols,
-                                                           float* __restrict__ out) {
+// caches they were just written to). The columns from `split` on go to `out2`; an
+// output that is null is left out.
+__global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ partials, int parts, int64_t cols,
+                                                           float* __restrict__ out, float* __restrict__ out2, int64_t split) {
   __shared__ float s[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
@@ -501,17 +605,25 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
       float t = s[0][lane];
 #pragma unroll
       for (int i = 1; i < 16; ++i) t += s[i][lane];
-      out[c] = t;
+      if (c < split) {
+        if (out) out[c] = t;
+      } else if (out2) {
+        out2[c - split] = t;
+      }
     }
     __syncthreads();
   }
 }
 
-hipError_t launch_column_sums(const float* partials, int parts, int cols, float* out, hipStream_t st) {
-  const int64_t want = ((int64_t)cols + 63) / 64;
+static hipError_t column_sums(const float* partials, int parts, int64_t cols, float* out, float* out2, int64_t split,
+                              hipStream_t st) {
+  const int64_t want = (cols + 63) / 64;
   hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)(want < (1 << 20) ? want : 1 << 20)), dim3(1024), 0, st, partials,
-                     parts, cols, out);
+                     parts, cols, out, out2, split);
   return hipGetLastError();
+}
+hipError_t launch_column_sums(const float* partials, int parts, int cols, float* out, hipStream_t st) {
+  return column_sums(partials, parts, cols, out, nullptr, cols, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -521,11 +633,11 @@ hipError_t launch_column_sums(const float* partials, int parts, int cols, float*
 // 2^32 threads).
 constexpr int64_t kMaxRowBlocks = 1 << 20;
 
-template <int XT, int WPR, int NV>
+template <bool LN, int XT, int WPR, int NV>
 static hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
   using C = NormFwd<XT, WPR, NV>;
   const int64_t want = ((int64_t)a.rows + C::kRows - 1) / C::kRows;
-  hipLaunchKernelGGL((rmsnorm_quant_kernel<XT, WPR, NV>), dim3((unsigned)(want < kMaxRowBlocks ? want : kMaxRowBlocks)),
+  hipLaunchKernelGGL((norm_quant_kernel<LN, XT, WPR, NV>), dim3((unsigned)(want < kMaxRowBlocks ? want : kMaxRowBlocks)),
                      dim3(C::kThreads), 0, st, a);
   return hipGetLastError();
 }
@@ -539,23 +651,27 @@ static hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
 // rows, whose latency counts (us, 7168 columns: one row 3.9 with 8 x 2 and 4.7
 // with 4 x 4, 4681 rows 53.2 and 51.1; 2048 columns: 1000 rows 4.8 with 4 x 1 and
 // 5.4 with 1 x 4, 16384 rows 53.0 and 49.3).
-template <int XT>
+template <bool LN, int XT>
 static hipError_t launch_norm_x(const NormArgs& a, hipStream_t st) {
   const int nvec = a.cols / VecTraits<XT>::kElems;
-  if (nvec <= 64 * 1) return launch_norm_t<XT, 1, 1>(a, st);
-  if (nvec <= 64 * 2) return launch_norm_t<XT, 1, 2>(a, st);
-  if (nvec <= 64 * 4) return a.rows < 4096 ? launch_norm_t<XT, 4, 1>(a, st) : launch_norm_t<XT, 1, 4>(a, st);
-  if (nvec <= 256 * 2) return launch_norm_t<XT, 4, 2>(a, st);
-  if (nvec <= 256 * 4) return a.rows < 1024 ? launch_norm_t<XT, 8, 2>(a, st) : launch_norm_t<XT, 4, 4>(a, st);
-  if (nvec <= 512 * 4) return launch_norm_t<XT, 8, 4>(a, st);
-  if (nvec <= 1024 * 4) return launch_norm_t<XT, 16, 4>(a, st);
-  hipLaunchKernelGGL((rmsnorm_quant_long_kernel<XT>), dim3((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)),
+  if (nvec <= 64 * 1) return launch_norm_t<LN, XT, 1, 1>(a, st);
+  if (nvec <= 64 * 2) return launch_norm_t<LN, XT, 1, 2>(a, st);
+  if (nvec <= 64 * 4) return a.rows < 4096 ? launch_norm_t<LN, XT, 4, 1>(a, st) : launch_norm_t<LN, XT, 1, 4>(a, st);
+  if (nvec <= 256 * 2) return launch_norm_t<LN, XT, 4, 2>(a, st);
+  if (nvec <= 256 * 4) return a.rows < 1024 ? launch_norm_t<LN, XT, 8, 2>(a, st) : launch_norm_t<LN, XT, 4, 4>(a, st);
+  if (nvec <= 512 * 4) return launch_norm_t<LN, XT, 8, 4>(a, st);
+  if (nvec <= 1024 * 4) return launch_norm_t<LN, XT, 16, 4>(a, st);
+  hipLaunchKernelGGL((norm_quant_long_kernel<LN, XT>), dim3((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)),
                      dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
 hipError_t launch_rmsnorm_quant(const NormArgs& a, int xt, hipStream_t st) {
-  return xt == kBF16 ? launch_norm_x<kBF16>(a, st) : launch_norm_x<kF32>(a, st);
+  return xt == kBF16 ? launch_norm_x<false, kBF16>(a, st) : launch_norm_x<false, kF32>(a, st);
+}
+
+hipError_t launch_layernorm_quant(const NormArgs& a, int xt, hipStream_t st) {
+  return xt == kBF16 ? launch_norm_x<true, kBF16>(a, st) : launch_norm_x<true, kF32>(a, st);
 }
 
 // dw without partial sums: few rows per slot, and tensors that the caches hold.
@@ -589,20 +705,21 @@ static BwdPlan bwd_plan(int rows, int cols, int xt) {
 size_t rmsnorm_bwd_workspace_bytes(int rows, int cols, int xt) {
   return (size_t)bwd_plan(rows, cols, xt).parts * (size_t)cols * 4;
 }
+size_t layernorm_bwd_workspace_bytes(int rows, int cols, int xt) { return 2 * rmsnorm_bwd_workspace_bytes(rows, cols, xt); }
 
-template <int XT, bool CKPT>
+template <bool LN, int XT, bool CKPT>
 static hipError_t launch_norm_bwd_t(NormBwdArgs a, hipStream_t st) {
   const BwdPlan p = bwd_plan(a.rows, a.cols, XT);
   const int nvec = a.cols / VecTraits<XT>::kElems;
   const dim3 block(1024);
-  const int dw_blocks = a.dw && p.direct ? (nvec + kColVecs - 1) / kColVecs : 0;
+  const int dw_blocks = (a.dw || a.db) && p.direct ? (nvec + kColVecs - 1) / kColVecs : 0;
   if (dw_blocks) a.partials = nullptr;
   const bool dw_first = dw_blocks && a.dx == a.dy;
 #define HQ_LAUNCH(WPR, NV)                                                                                               \
   do {                                                                                                                   \
     if (dw_first)                                                                                                        \
-      hipLaunchKernelGGL((rmsnorm_bwd_kernel<XT, WPR, NV, CKPT>), dim3(dw_blocks), block, 0, st, a, 0);                  \
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<XT, WPR, NV, CKPT>), dim3(p.parts + (dw_first ? 0 : dw_blocks)), block, 0, st, \
+      hipLaunchKernelGGL((norm_bwd_kernel<LN, XT, WPR, NV, CKPT>), dim3(dw_blocks), block, 0, st, a, 0);                  \
+    hipLaunchKernelGGL((norm_bwd_kernel<LN, XT, WPR, NV, CKPT>), dim3(p.parts + (dw_first ? 0 : dw_blocks)), block, 0, st, \
                        a, p.parts);                                                                                      \
   } while (0)
   if (p.wpr == 1) HQ_LAUNCH(1, 1);
@@ -613,23 +730,27 @@ static hipError_t launch_norm_bwd_t(NormBwdArgs a, hipStream_t st) {
   else {
     // dw first: dx may be dy's own buffer
     if (a.partials) {
-      hipLaunchKernelGGL((rmsnorm_bwd_dw_long_kernel<XT, CKPT>), dim3((nvec + 1023) / 1024, p.parts), block, 0, st, a);
+      hipLaunchKernelGGL((norm_bwd_dw_long_kernel<LN, XT, CKPT>), dim3((nvec + 1023) / 1024, p.parts), block, 0, st, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((rmsnorm_bwd_dx_long_kernel<XT, CKPT>), dim3(a.rows < kNumCUs * 2 ? a.rows : kNumCUs * 2), block, 0,
+    hipLaunchKernelGGL((norm_bwd_dx_long_kernel<LN, XT, CKPT>), dim3(a.rows < kNumCUs * 2 ? a.rows : kNumCUs * 2), block, 0,
                        st, a);
   }
 #undef HQ_LAUNCH
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.partials) return e;
-  return launch_column_sums(a.partials, p.parts, a.cols, a.dw, st);
+  return column_sums(a.partials, p.parts, (LN ? 2 : 1) * (int64_t)a.cols, a.dw, a.db, a.cols, st);
 }
 
-hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st) {
-  if (a.rows == 0) return a.dw ? launch_column_sums(nullptr, 0, a.cols, a.dw, st) : hipSuccess;
-  if (xt == kBF16) return a.cq ? launch_norm_bwd_t<kBF16, true>(a, st) : launch_norm_bwd_t<kBF16, false>(a, st);
-  return a.cq ? launch_norm_bwd_t<kF32, true>(a, st) : launch_norm_bwd_t<kF32, false>(a, st);
+template <bool LN>
+static hipError_t launch_norm_bwd(const NormBwdArgs& a, int xt, hipStream_t st) {
+  if (a.rows == 0) return a.dw || a.db ? column_sums(nullptr, 0, (LN ? 2 : 1) * (int64_t)a.cols, a.dw, a.db, a.cols, st) : hipSuccess;
+  if (xt == kBF16) return a.cq ? launch_norm_bwd_t<LN, kBF16, true>(a, st) : launch_norm_bwd_t<LN, kBF16, false>(a, st);
+  return a.cq ? launch_norm_bwd_t<LN, kF32, true>(a, st) : launch_norm_bwd_t<LN, kF32, false>(a, st);
 }
+
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st) { return launch_norm_bwd<false>(a, xt, st); }
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int xt, hipStream_t st) { return launch_norm_bwd<true>(a, xt, st); }
 
 }  // namespace hq

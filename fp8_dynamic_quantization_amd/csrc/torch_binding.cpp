@@ -248,6 +248,85 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// x, weight, bias, eps, fmt, residual, h, write_h, ckpt q, ckpt scales, block_size, q, scale, mean, rstd
+//   -> q, scale, h, mean, rstd, ckpt q, ckpt scales
+PyObject* layernorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 15);
+  const Tensor x0 = tensor(a[0], "x"), w0 = maybe(a[1], "weight"), b0 = maybe(a[2], "bias"), res0 = maybe(a[5], "residual");
+  const float eps = (float)real(a[3]);
+  const int fmt = (int)integer(a[4]);
+  const bool write_h = a[7] == Py_True;
+  const int64_t block = integer(a[10]);
+  const Tensor cq = maybe(a[8], "checkpoint.q"), cs = maybe(a[9], "checkpoint.scales");
+  Tensor h = maybe(a[6], "h"), q = maybe(a[11], "q"), s = maybe(a[12], "scale_out"), m = maybe(a[13], "mean_out");
+  Tensor r = maybe(a[14], "rstd_out");
+  Ckpt k;
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(x0, "x");
+    const Tensor x = x0.contiguous();
+    const ScalarType dt = x.scalar_type();
+    const int64_t rows = x.size(0), cols = x.size(1);
+    const Tensor w = input(w0, {cols}, dt, x, "weight");
+    const Tensor b = input(b0, {cols}, dt, x, "bias");
+    const Tensor res = input(res0, {rows, cols}, dt, x, "residual");
+    const c10::OptionalDeviceGuard guard(x.device());
+    h = write_h ? output(h, {rows, cols}, dt, x, "h") : Tensor();
+    k = checkpoint_out(cq, cs, block, rows, cols, x);
+    q = output(q, {rows, cols}, ScalarType::Byte, x, "q");
+    s = output(s, {rows}, ScalarType::Float, x, "scale_out");
+    m = output(m, {rows}, ScalarType::Float, x, "mean_out");
+    r = output(r, {rows}, ScalarType::Float, x, "rstd_out");
+    on_gpu(x, "x");
+    st = hq_layernorm_quantize_fp8(ptr(x), ptr(res), ptr(w), ptr(b), xt, rows, cols, eps, fmt, ptr<uint8_t>(q), ptr<float>(s),
+                                   ptr(h), ptr<float>(m), ptr<float>(r), k.p(), stream_of(x));
+  }
+  raise_unless_ok(st);
+  return wrap_all(q, s, h, m, r, k.q, k.scales);
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, h, ckpt q, ckpt scales, block_size, weight, mean, rstd, dresidual, dx, dweight, want_dweight, dbias, want_dbias,
+// workspace -> dx, dweight, dbias
+PyObject* layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 15);
+  const Tensor dy0 = tensor(a[0], "dy"), h0 = maybe(a[1], "h"), w0 = maybe(a[5], "weight"), mean0 = tensor(a[6], "mean");
+  const Tensor rstd0 = tensor(a[7], "rstd"), dr0 = maybe(a[8], "dresidual"), given = maybe(a[14], "workspace");
+  const int64_t block = integer(a[4]);
+  const Tensor cq = maybe(a[2], "checkpoint.q"), cs = maybe(a[3], "checkpoint.scales");
+  const bool want_w = a[11] == Py_True, want_b = a[13] == Py_True;
+  Tensor dx = maybe(a[9], "dx"), dw = maybe(a[10], "dweight"), db = maybe(a[12], "dbias");
+  hq_status st;
+  {
+    const NoGil nogil;
+    const int xt = real_type(dy0, "dy");
+    const Tensor dy = dy0.contiguous();
+    const ScalarType dt = dy.scalar_type();
+    const int64_t rows = dy.size(0), cols = dy.size(1);
+    const Tensor h = input(h0, {rows, cols}, dt, dy, "h");
+    const Ckpt k = checkpoint_in(cq, cs, block, rows, cols, dy);
+    const Tensor w = input(w0, {cols}, dt, dy, "weight");
+    const Tensor mean = input(mean0, {rows}, ScalarType::Float, dy, "mean");
+    const Tensor rstd = input(rstd0, {rows}, ScalarType::Float, dy, "rstd");
+    const Tensor dr = input(dr0, {rows, cols}, dt, dy, "dresidual");
+    check_workspace(given, dy);
+    const c10::OptionalDeviceGuard guard(dy.device());
+    dx = output(dx, {rows, cols}, dt, dy, "dx");
+    dw = want_w ? output(dw, {cols}, ScalarType::Float, dy, "dweight") : Tensor();
+    db = want_b ? output(db, {cols}, ScalarType::Float, dy, "dbias") : Tensor();
+    on_gpu(dy, "dy");
+    const Tensor ws = scratch(given, want_w || want_b, hq_layernorm_backward_workspace_bytes(xt, rows, cols), dy);
+    st = hq_layernorm_backward(ptr(dy), ptr(h), k.p(), ptr(w), ptr<float>(mean), ptr<float>(rstd), ptr(dr), xt, rows, cols,
+                               ptr(dx), ptr<float>(dw), ptr<float>(db), ptr(ws), bytes_of(ws), stream_of(dy));
+  }
+  raise_unless_ok(st);
+  return wrap_all(dx, dw, db);
+  END_HANDLE_TH_ERRORS
+}
+
 // xq, xf, wq_pre, wf, x_scale, w_scale, n, bias, bias_type, bias_scale, act, residual, out_scale, out_fmt, out,
 // workspace (None: the shared one, False: none) -> out
 PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
@@ -431,6 +510,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define HQ_METHOD(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(F)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {HQ_METHOD(setup),        HQ_METHOD(rmsnorm_quantize), HQ_METHOD(rmsnorm_backward), HQ_METHOD(gemm_fused),
+                         HQ_METHOD(layernorm_quantize), HQ_METHOD(layernorm_backward),
                          HQ_METHOD(act_quantize), HQ_METHOD(act_backward),     HQ_METHOD(wgrad),            HQ_METHOD(capture_id),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hqtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

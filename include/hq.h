@@ -570,6 +570,42 @@ hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint
                               const float* rstd, const void* dresidual, int xt, int64_t rows, int64_t cols, void* dx,
                               float* dweight, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Layer norm with the residual's addition, into per-token FP8 codes:
+ *   h    = x + residual                        (x without a residual)
+ *   mean = mean_c(h), rstd = 1 / sqrt(mean_c((h - mean)^2) + eps)
+ *   y    = fl32(fl32((h - mean) * rstd) * weight) + bias
+ *   q, scale_out = the per-token quantization of y, as hq_quantize_fp8
+ * h is used unrounded, and the squares are summed of the differences. A NaN or an Inf
+ * in a row, and a row whose sum passes float32's range, make the row's codes 0x7F and
+ * its scale 2^-126; squares whose sum passes the range make rstd 0 and y the bias.
+ *   bias       device, [cols] of xt, or NULL for zeros
+ *   mean_out   device, float32 [rows], or NULL (the backward pass needs it)
+ * All other arguments, and the requirements, are those of hq_rmsnorm_quantize_fp8.
+ * Rows of up to 32768 bf16 (16384 float32) elements are read once, longer ones four
+ * times. */
+hq_status hq_layernorm_quantize_fp8(const void* x, const void* residual, const void* weight, const void* bias, int xt,
+                                    int64_t rows, int64_t cols, float eps, int fmt, uint8_t* q, float* scale_out,
+                                    void* h_out, float* mean_out, float* rstd_out, const hq_checkpoint* ckpt,
+                                    hipStream_t stream);
+
+/* Bytes of device workspace hq_layernorm_backward needs for dweight or dbias: partial
+ * sums of both, [<= 256, 2 * cols] float32. 0 for arguments that it refuses. */
+size_t hq_layernorm_backward_workspace_bytes(int xt, int64_t rows, int64_t cols);
+
+/* Backward pass of that norm. With xh = (h - mean) * rstd and t = dy * weight:
+ *   dx      = rstd * (t - mean_c(t) - xh * mean_c(t * xh)) + dresidual
+ *   dweight = sum over rows of dy * xh
+ *   dbias   = sum over rows of dy
+ *   mean       device, float32 [rows], as the forward pass wrote it
+ *   dbias      device, float32 [cols], 16-byte aligned, or NULL
+ *   workspace  may be NULL without dweight and dbias
+ * All other arguments, the order of the sums and the requirements are those of
+ * hq_rmsnorm_backward. rows == 0 writes zeros to dweight and dbias. */
+hq_status hq_layernorm_backward(const void* dy, const void* h, const hq_checkpoint* ckpt, const void* weight,
+                                const float* mean, const float* rstd, const void* dresidual, int xt, int64_t rows,
+                                int64_t cols, void* dx, float* dweight, float* dbias, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
 /* Options of the fused epilogue (host struct): those of hq_epilogue, then
  *   act       an hq_act value
  *   residual  device bf16 [m, n], 16-byte aligned, or NULL for none */

@@ -5,6 +5,9 @@ Oracle (test infrastructure only; see the package docstring).
   rmsnorm           h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * weight
   rmsnorm_backward  xh = h * rstd, t = dy * weight: dx = dres + rstd * (t - xh * mean(t * xh)),
                     dweight = sum over rows of dy * xh
+  layernorm         d = h - mean(h), rstd = 1 / sqrt(mean(d^2) + eps), y = d * rstd * weight + bias
+  layernorm_backward  xh = d * rstd, t = dy * weight: dx = dres + rstd * (t - mean(t) - xh * mean(t * xh)),
+                    dweight = sum over rows of dy * xh, dbias = sum over rows of dy
   act, act_grad     ReLU, GELU (x Phi(x)), its tanh approximation, SiLU, and their derivatives
   act_forward       act(z) or, gated, act(z1) * z2 with z = [z1 | z2]
   act_backward      the gradient of that with respect to z
@@ -49,6 +52,34 @@ def rmsnorm_backward(dy, h, weight, rstd, dresidual=None):
         dx = dx + dresidual
         a = a + np.abs(dresidual)
     return dx, (dy * xh).sum(axis=0), a, np.abs(dy * xh).sum(axis=0)
+
+
+def layernorm(x, weight, bias, eps, residual=None):
+    """(h, mean [rows], rstd [rows], y) of float64 arrays; weight None is ones, bias None zeros."""
+    h = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
+    mean = h.mean(axis=1)
+    d = h - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(axis=1) + eps)
+    y = d * rstd[:, None]
+    if weight is not None:
+        y = y * np.asarray(weight, np.float64)
+    return h, mean, rstd, y if bias is None else y + np.asarray(bias, np.float64)
+
+
+def layernorm_backward(dy, h, weight, mean, rstd, dresidual=None):
+    """(dx, dweight, dbias, abs_dx, abs_dw, abs_db): the gradients and the sums of absolute
+    terms, in which h and the mean count apart (a difference of them may be small)."""
+    dy, h, mean, rstd = (np.asarray(v, np.float64) for v in (dy, h, mean, rstd))
+    mean, rstd = mean[:, None], rstd[:, None]
+    xh, xa = (h - mean) * rstd, (np.abs(h) + np.abs(mean)) * rstd
+    t = dy if weight is None else dy * np.asarray(weight, np.float64)
+    dx = rstd * (t - t.mean(axis=1, keepdims=True) - xh * (t * xh).mean(axis=1, keepdims=True))
+    ta = np.abs(t)
+    a = rstd * (ta + ta.mean(axis=1, keepdims=True) + xa * (ta * xa).mean(axis=1, keepdims=True))
+    if dresidual is not None:
+        dx = dx + dresidual
+        a = a + np.abs(dresidual)
+    return dx, (dy * xh).sum(axis=0), dy.sum(axis=0), a, (np.abs(dy) * xa).sum(axis=0), np.abs(dy).sum(axis=0)
 
 
 def act(kind, z):
