@@ -5,10 +5,12 @@ include/hq.h); this package is its thin Python binding.
 """
 from ._lib import (HQ_ACT_GELU, HQ_ACT_GELU_TANH, HQ_ACT_NONE, HQ_ACT_RELU, HQ_ACT_SILU, HQ_BF16, HQ_BIAS_BF16, HQ_BIAS_E4M3, HQ_BIAS_E5M2, HQ_E4M3, HQ_E5M2, HQ_ERR_INVALID_ARGUMENT, HQ_ERR_LAUNCH,
                    HQ_ERR_UNSUPPORTED_DEVICE, HQ_F32, HQ_OK, HQ_PER_CHANNEL, HQ_PER_TENSOR,
-                   HQ_PER_TOKEN, HQError, HQInvalidArgument, HQLaunchError,
-                   HQUnsupportedDevice, LIB_PATH, SIGNATURES, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_ring, load)
+                   HQ_PER_TOKEN, HQ_ROUTE_SIGMOID, HQ_ROUTE_SOFTMAX, HQError, HQInvalidArgument, HQLaunchError,
+                   HQUnsupportedDevice, LIB_PATH, SIGNATURES, hq_checkpoint, hq_epilogue, hq_fused_epilogue, hq_moe_layer,
+                   hq_ring, load)
 from .api import (Checkpoint, LayerNormQuantized, RmsNormQuantized, Ring, hq_act_backward, hq_act_backward_workspace_bytes, hq_act_quantize_fp8,
                   hq_gemm_a8w8_fused, hq_layernorm_backward, hq_layernorm_backward_workspace_bytes, hq_layernorm_quantize_fp8,
+                  hq_moe_a8w8, hq_moe_route, hq_moe_route_backward, hq_moe_workspace_bytes,
                   hq_rmsnorm_backward, hq_rmsnorm_backward_workspace_bytes, hq_rmsnorm_quantize_fp8,
                   hq_wgrad_a8, hq_wgrad_a8_strict, hq_wgrad_workspace_bytes, gemm_workspace, hq_gemm_a8w8, hq_gemm_a8w8_blockscaled, hq_gemm_a8w8_epilogue,
                   hq_gemm_a8w8_blockscaled_preshuffled,
@@ -37,4 +39,6 @@ __all__ = [
     "hq_rmsnorm_backward_workspace_bytes", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward",
     "hq_act_backward_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict", "hq_wgrad_workspace_bytes",
     "LayerNormQuantized", "hq_layernorm_quantize_fp8", "hq_layernorm_backward", "hq_layernorm_backward_workspace_bytes",
+    "HQ_ROUTE_SOFTMAX", "HQ_ROUTE_SIGMOID", "hq_moe_layer", "hq_moe_route", "hq_moe_route_backward", "hq_moe_workspace_bytes",
+    "hq_moe_a8w8",
 ]

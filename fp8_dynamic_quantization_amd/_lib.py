@@ -30,6 +30,8 @@ HQ_ACT_RELU = 1
 HQ_ACT_GELU = 2
 HQ_ACT_GELU_TANH = 3
 HQ_ACT_SILU = 4
+HQ_ROUTE_SOFTMAX = 0
+HQ_ROUTE_SIGMOID = 1
 
 
 class hq_ring(ctypes.Structure):
@@ -53,6 +55,14 @@ class hq_fused_epilogue(ctypes.Structure):
 
 class hq_checkpoint(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block_size", ctypes.c_int32)]
+
+
+class hq_moe_layer(ctypes.Structure):
+    _fields_ = [("w1_pre", ctypes.c_void_p), ("w1_scale", ctypes.c_void_p), ("w1_scale_count", ctypes.c_int64),
+                ("bias1", ctypes.c_void_p), ("w2_pre", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
+                ("w2_scale_count", ctypes.c_int64), ("bias2", ctypes.c_void_p), ("hidden", ctypes.c_int64),
+                ("inner", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("wf", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("gated", ctypes.c_int32)]
 
 
 class HQError(RuntimeError):
@@ -130,6 +140,10 @@ SIGNATURES = {
     "hq_wgrad_workspace_bytes": (_I64, [_I64, _I64, _I64, _I]),
     "hq_wgrad_a8": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
     "hq_wgrad_a8_strict": (_I, [_P, _P, _I, _P, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
+    "hq_moe_route": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _P, _P, _P]),
+    "hq_moe_route_backward": (_I, [_P, _P, _P, _I, _I64, _I64, _I, _I, _I, _P, _P]),
+    "hq_moe_workspace_bytes": (_I64, [_I64, _I, _I64, _I64, _I64]),
+    "hq_moe_a8w8": (_I, [_P, _I, _P, _I64, _P, _P, _I64, _I, ctypes.POINTER(hq_moe_layer), _P, _P, _P, _SZ, _P]),
     "hq_last_error": (ctypes.c_char_p, []),
 }
 

@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import (HQ_ACT_NONE, HQ_BF16, HQ_BIAS_BF16, HQ_E4M3, HQ_E5M2, HQ_F32, HQ_PER_CHANNEL, HQ_PER_TENSOR,
-                   HQ_PER_TOKEN, check, hq_epilogue, hq_ring, load)
+                   HQ_PER_TOKEN, HQ_ROUTE_SOFTMAX, check, hq_epilogue, hq_ring, load)
 
 __all__ = [
     "Ring", "hq_scale_count", "hq_quantize_workspace_bytes", "hq_preshuffled_bytes",
@@ -34,6 +34,7 @@ __all__ = [
     "hq_rmsnorm_backward", "hq_gemm_a8w8_fused", "hq_act_quantize_fp8", "hq_act_backward_workspace_bytes",
     "hq_act_backward", "hq_wgrad_workspace_bytes", "hq_wgrad_a8", "hq_wgrad_a8_strict",
     "LayerNormQuantized", "hq_layernorm_quantize_fp8", "hq_layernorm_backward_workspace_bytes", "hq_layernorm_backward",
+    "hq_moe_route", "hq_moe_route_backward", "hq_moe_workspace_bytes", "hq_moe_a8w8",
 ]
 
 _XT = {torch.float32: HQ_F32, torch.bfloat16: HQ_BF16}
@@ -765,3 +766,61 @@ def hq_wgrad_a8(g: torch.Tensor, xq: torch.Tensor, xf: int, x_scale: torch.Tenso
 def hq_wgrad_a8_strict(*args, **kwargs) -> torch.Tensor:
     """hq_wgrad_a8 with every term in two numbers, whatever the result's type; same arguments."""
     return hq_wgrad_a8(*args, strict=True, **kwargs)
+
+
+# ---------------------------------------------------------------------------
+# mixture of experts
+# ---------------------------------------------------------------------------
+def hq_moe_route(logits: torch.Tensor, topk: int, *, score: int = HQ_ROUTE_SOFTMAX, renormalize: bool = True, ids=None,
+                 weights=None, stream=None):
+    """The topk experts of each token by its logits [tokens, experts] (equal logits: the
+    lower index): returns (ids int32 [tokens, topk], weights float32 [tokens, topk]).
+    `score`: HQ_ROUTE_SOFTMAX (over all experts) or HQ_ROUTE_SIGMOID; `renormalize`
+    divides by the chosen scores' sum. Experts with logits of -Inf or NaN are never
+    chosen; slots left over have id -1 and weight 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_moe_route(logits, topk, score=score, renormalize=renormalize, ids=ids, weights=weights)
+    return _native().moe_route(logits, topk, score, bool(renormalize), ids, weights)
+
+
+def hq_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, *, score: int = HQ_ROUTE_SOFTMAX,
+                          renormalize: bool = True, dlogits=None, stream=None) -> torch.Tensor:
+    """Backward pass of hq_moe_route: the gradient of the logits [tokens, experts] from
+    that of the weights [tokens, topk], the choice `ids` held fixed."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_moe_route_backward(logits, ids, dweights, score=score, renormalize=renormalize, dlogits=dlogits)
+    return _native().moe_route_backward(logits, ids, dweights, score, bool(renormalize), dlogits)
+
+
+def hq_moe_workspace_bytes(tokens: int, topk: int, num_experts: int, hidden: int, inner: int) -> int:
+    return int(load().hq_moe_workspace_bytes(tokens, topk, num_experts, hidden, inner))
+
+
+def hq_moe_a8w8(xq: torch.Tensor, xf: int, x_scale: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                w1_pre: torch.Tensor, w1_scale: torch.Tensor, w2_pre: torch.Tensor, w2_scale: torch.Tensor, wf: int, *,
+                act: int, gated: bool = False, inner: int | None = None, bias1: torch.Tensor | None = None,
+                bias2: torch.Tensor | None = None, residual: torch.Tensor | None = None, out=None, workspace=None,
+                stream=None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for at most 64 tokens: bf16 [tokens, hidden] =
+    sum_j weights[t, j] (W2[e] a + bias2[e]) + residual[t], e = ids[t, j], with
+    a = act(z) or, gated, act(z[:inner]) * z[inner:], z = W1[e] x[t] + bias1[e].
+
+    `xq` are codes [tokens, hidden] with `x_scale` [tokens] (or [1]); `w1_pre` and
+    `w2_pre` the experts' pre-shuffled codes, one after the other, of [inner, hidden]
+    (gated [2 * inner, hidden]) and [hidden, inner], as hq_grouped_gemm_a8w8 takes them;
+    their scales [experts, rows] or [experts]. `inner` is taken from `w1_scale` unless
+    that has one scale per expert. Biases are bf16 [experts, rows]. Slots whose id is no
+    expert add nothing. `out` may be the residual itself. `workspace`: None (the
+    stream's shared one) or a uint8 tensor that was zero-filled once."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_moe_a8w8(xq, xf, x_scale, ids, weights, w1_pre, w1_scale, w2_pre, w2_scale, wf, act=act, gated=gated,
+                               inner=inner, bias1=bias1, bias2=bias2, residual=residual, out=out, workspace=workspace)
+    if inner is None:
+        if w1_scale.dim() != 2:
+            raise ValueError("inner must be given where w1_scale has one scale per expert")
+        inner = w1_scale.shape[1] // 2 if gated else w1_scale.shape[1]
+    return _native().moe(xq, xf, x_scale, ids, weights, w1_pre, w1_scale, w2_pre, w2_scale, wf, inner, act, bool(gated), bias1,
+                         bias2, residual, out, workspace)

@@ -23,13 +23,13 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhq.so")
 BINDING = os.path.join(PKG, "_hqtorch.so")
 
-SOURCES = ["quantize.hip", "gemm.hip", "gemm_fused.hip", "blockscaled.hip", "norm.hip", "act.hip", "wgrad.hip", "probe.hip",
+SOURCES = ["quantize.hip", "gemm.hip", "gemm_fused.hip", "blockscaled.hip", "norm.hip", "act.hip", "wgrad.hip", "moe.hip", "probe.hip",
            "hq_api.cpp"]
 
 # Per-source flags. The GEMM keeps its MFMA accumulators in VGPRs and the
 # operand fragments in AGPRs: with 256 accumulator registers per wavefront the
 # default AGPR-accumulator allocation spills to scratch, this form does not.
-EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("gemm.hip", "gemm_fused.hip", "blockscaled.hip", "wgrad.hip")}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("gemm.hip", "gemm_fused.hip", "blockscaled.hip", "wgrad.hip", "moe.hip")}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

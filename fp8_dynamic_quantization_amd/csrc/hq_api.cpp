@@ -1133,4 +1133,129 @@ hq_status hq_wgrad_a8_strict(const uint16_t* g, const uint8_t* xq, int xf, const
                     "hq_wgrad_a8_strict", stream);
 }
 
+// The router, forward and backward.
+static hq_status check_route(int xt, int64_t tokens, int64_t experts, int topk, int score, int renormalize) {
+  if (xt != HQ_F32 && xt != HQ_BF16) return fail(HQ_ERR_INVALID_ARGUMENT, "xt must be HQ_F32 or HQ_BF16, got %d", xt);
+  if (tokens < 0 || tokens > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "tokens must be in [0, 2^31 - 1024], got %lld", (long long)tokens);
+  if (experts < 1 || experts > 1024)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "num_experts must be in [1, 1024], got %lld", (long long)experts);
+  if (topk < 1 || topk > 16 || topk > experts)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "topk must be in [1, min(16, num_experts)], got %d", topk);
+  if (score != HQ_ROUTE_SOFTMAX && score != HQ_ROUTE_SIGMOID)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "score must be HQ_ROUTE_SOFTMAX or HQ_ROUTE_SIGMOID, got %d", score);
+  if (renormalize != 0 && renormalize != 1) return fail(HQ_ERR_INVALID_ARGUMENT, "renormalize must be 0 or 1, got %d", renormalize);
+  return HQ_OK;
+}
+
+hq_status hq_moe_route(const void* logits, int xt, int64_t tokens, int64_t num_experts, int topk, int score,
+                       int renormalize, int32_t* ids, float* weights, hipStream_t stream) {
+  hq_status st = check_route(xt, tokens, num_experts, topk, score, renormalize);
+  if (st != HQ_OK) return st;
+  if (tokens == 0) return ok();
+  if (!logits || !ids || !weights) return fail(HQ_ERR_INVALID_ARGUMENT, "logits, ids and weights must be non-NULL");
+  const size_t es = xt == HQ_BF16 ? 2 : 4, slots = (size_t)tokens * (size_t)topk * 4;
+  if (!aligned(logits, es) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "logits must be aligned to its elements, ids and weights to 4 bytes");
+  const Range rg[] = {{ids, slots, "ids"}, {weights, slots, "weights"}, {logits, (size_t)tokens * (size_t)num_experts * es, "logits"}};
+  st = check_outputs(rg, 3, 2);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::RouteArgs a{logits, ids, weights, (int)tokens, (int)num_experts, topk, score, renormalize};
+  return launched(hq::launch_moe_route(a, xt, stream), "hq_moe_route");
+}
+
+hq_status hq_moe_route_backward(const void* logits, const int32_t* ids, const float* dweights, int xt, int64_t tokens,
+                                int64_t num_experts, int topk, int score, int renormalize, void* dlogits,
+                                hipStream_t stream) {
+  hq_status st = check_route(xt, tokens, num_experts, topk, score, renormalize);
+  if (st != HQ_OK) return st;
+  if (tokens == 0) return ok();
+  if (!logits || !ids || !dweights || !dlogits)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "logits, ids, dweights and dlogits must be non-NULL");
+  const size_t es = xt == HQ_BF16 ? 2 : 4, slots = (size_t)tokens * (size_t)topk * 4, all = (size_t)tokens * (size_t)num_experts * es;
+  if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 4) || !aligned(dweights, 4))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "logits and dlogits must be aligned to their elements, ids and dweights to 4 bytes");
+  const Range rg[] = {{dlogits, all, "dlogits"}, {logits, all, "logits"}, {ids, slots, "ids"}, {dweights, slots, "dweights"}};
+  st = check_outputs(rg, 4, 1);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::RouteBwdArgs a{logits, ids, dweights, dlogits, (int)tokens, (int)num_experts, topk, score, renormalize};
+  return launched(hq::launch_moe_route_bwd(a, xt, stream), "hq_moe_route_backward");
+}
+
+static bool moe_sizes(int64_t tokens, int topk, int64_t experts, int64_t hidden, int64_t inner) {
+  return tokens >= 0 && tokens <= 64 && topk >= 1 && topk <= 16 && experts >= 1 && experts <= 1024 && hidden >= 16 &&
+         hidden <= 65536 && hidden % 16 == 0 && inner >= 16 && inner <= 65536 && inner % 16 == 0;
+}
+
+int64_t hq_moe_workspace_bytes(int64_t tokens, int topk, int64_t num_experts, int64_t hidden, int64_t inner) {
+  if (!moe_sizes(tokens, topk, num_experts, hidden, inner)) return -1;
+  if (tokens == 0) return 0;
+  return (int64_t)hq::moe_workspace_bytes((int)tokens, topk, (int)num_experts, (int)hidden, (int)inner);
+}
+
+hq_status hq_moe_a8w8(const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count, const int32_t* ids,
+                      const float* weights, int64_t tokens, int topk, const hq_moe_layer* layer, const uint16_t* residual,
+                      uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!layer) return fail(HQ_ERR_INVALID_ARGUMENT, "layer must be non-NULL");
+  const hq_moe_layer& l = *layer;
+  if (!valid_fmt(xf) || !valid_fmt(l.wf)) return fail(HQ_ERR_INVALID_ARGUMENT, "xf and wf must be HQ_E4M3 or HQ_E5M2");
+  if (!valid_act(l.act)) return fail(HQ_ERR_INVALID_ARGUMENT, "unknown activation %d", l.act);
+  if (l.gated != 0 && l.gated != 1) return fail(HQ_ERR_INVALID_ARGUMENT, "gated must be 0 or 1, got %d", l.gated);
+  if (!moe_sizes(tokens, topk, l.num_experts, l.hidden, l.inner) || (l.gated && l.inner % 32 != 0))
+    return fail(HQ_ERR_INVALID_ARGUMENT,
+                "tokens must be in [0, 64], topk in [1, 16], num_experts in [1, 1024], hidden and inner multiples of 16 (gated: "
+                "inner of 32) up to 65536, got %lld, %d, %d, %lld, %lld", (long long)tokens, topk, l.num_experts,
+                (long long)l.hidden, (long long)l.inner);
+  const int64_t experts = l.num_experts, n1 = l.gated ? 2 * l.inner : l.inner;
+  if (x_scale_count != 1 && x_scale_count != tokens)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x_scale_count must be 1 or tokens (%lld), got %lld", (long long)tokens,
+                (long long)x_scale_count);
+  if ((l.w1_scale_count != experts && l.w1_scale_count != experts * n1) ||
+      (l.w2_scale_count != experts && l.w2_scale_count != experts * l.hidden))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "a weight's scale count must be num_experts or num_experts times its rows, got %lld, %lld",
+                (long long)l.w1_scale_count, (long long)l.w2_scale_count);
+  if (tokens == 0) return ok();
+  if (!xq || !x_scale || !ids || !weights || !l.w1_pre || !l.w1_scale || !l.w2_pre || !l.w2_scale || !out)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "xq, x_scale, ids, weights, both weights, their scales and out must be non-NULL");
+  if (!aligned(xq, 16) || !aligned(l.w1_pre, 16) || !aligned(l.w2_pre, 16) || !aligned(residual, 16) || !aligned(out, 16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "xq, w1_pre, w2_pre, residual and out must be 16-byte aligned");
+  if (!aligned(x_scale, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(l.w1_scale, 4) || !aligned(l.w2_scale, 4) ||
+      !aligned(l.bias1, 2) || !aligned(l.bias2, 2))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "ids, weights and scales must be 4-byte, biases 2-byte aligned");
+  const size_t need = hq::moe_workspace_bytes((int)tokens, topk, (int)experts, (int)l.hidden, (int)l.inner);
+  hq_status st = check_sum_workspace(workspace, workspace_bytes, need);
+  if (st != HQ_OK) return st;
+  const size_t slots = (size_t)tokens * (size_t)topk * 4, rows = (size_t)tokens * (size_t)l.hidden;
+  const Range rg[] = {
+      {out, rows * 2, "out"},
+      {workspace, need, "workspace"},
+      {xq, rows, "xq"},
+      {x_scale, (size_t)x_scale_count * 4, "x_scale"},
+      {ids, slots, "ids"},
+      {weights, slots, "weights"},
+      {l.w1_pre, (size_t)padded_bytes(n1, l.hidden) * (size_t)experts, "w1_pre"},
+      {l.w1_scale, (size_t)l.w1_scale_count * 4, "w1_scale"},
+      {l.bias1, (size_t)experts * (size_t)n1 * 2, "bias1"},
+      {l.w2_pre, (size_t)padded_bytes(l.hidden, l.inner) * (size_t)experts, "w2_pre"},
+      {l.w2_scale, (size_t)l.w2_scale_count * 4, "w2_scale"},
+      {l.bias2, (size_t)experts * (size_t)l.hidden * 2, "bias2"},
+      {residual == out ? nullptr : residual, rows * 2, "residual"},
+  };
+  st = check_outputs(rg, 13, 2);
+  if (st != HQ_OK) return st;
+  st = check_device();
+  if (st != HQ_OK) return st;
+  (void)hipGetLastError();
+  const hq::MoeArgs a{xq, x_scale, ids, weights, l.w1_pre, l.w1_scale, l.bias1, l.w2_pre, l.w2_scale, l.bias2, residual, out,
+                      nullptr, (int)tokens, topk, (int)experts, (int)l.hidden, (int)l.inner, x_scale_count != 1,
+                      l.w1_scale_count != experts, l.w2_scale_count != experts};
+  return launched(hq::launch_moe(a, xf, l.wf, l.act, l.gated != 0, workspace, stream), "hq_moe_a8w8");
+}
+
 }  // extern "C"

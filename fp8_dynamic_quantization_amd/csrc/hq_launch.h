@@ -228,6 +228,48 @@ struct ActBwdArgs {
 size_t act_bwd_workspace_bytes(int rows, int cols, int xt, bool gated);
 hipError_t launch_act_bwd(const ActBwdArgs& a, int xt, int act, bool gated, hipStream_t st);
 
+// Expert router: the topk largest logits of each token.
+constexpr int kRouteSoftmax = 0, kRouteSigmoid = 1;
+struct RouteArgs {
+  const void* logits;  // [tokens, experts]
+  int32_t* ids;        // [tokens, topk]
+  float* weights;      // [tokens, topk]
+  int tokens, experts, topk, score, renormalize;
+};
+hipError_t launch_moe_route(const RouteArgs& a, int xt, hipStream_t st);
+
+struct RouteBwdArgs {
+  const void* logits;     // [tokens, experts]
+  const int32_t* ids;     // [tokens, topk]
+  const float* dweights;  // [tokens, topk]
+  void* dlogits;          // [tokens, experts]
+  int tokens, experts, topk, score, renormalize;
+};
+hipError_t launch_moe_route_bwd(const RouteBwdArgs& a, int xt, hipStream_t st);
+
+// Mixture-of-experts layer of a few tokens. Weights are pre-shuffled, expert after
+// expert: W1 [inner, hidden], gated [2 inner, hidden]; W2 [hidden, inner].
+struct MoeArgs {
+  const uint8_t* xq;      // [tokens, hidden]
+  const float* x_scale;   // [1] or [tokens]
+  const int32_t* ids;     // [tokens, topk]
+  const float* weights;   // [tokens, topk]
+  const uint8_t* w1;
+  const float* s1;        // [experts], or per column of W1's output
+  const uint16_t* b1;     // bf16, per column, or null
+  const uint8_t* w2;
+  const float* s2;
+  const uint16_t* b2;
+  const uint16_t* residual;  // bf16 [tokens, hidden] or null
+  uint16_t* out;             // bf16 [tokens, hidden]
+  uint16_t* a;               // bf16 [tokens * topk, inner], in the workspace (the launcher sets it)
+  int tokens, topk, experts, hidden, inner;
+  int x_scale_per_row, s1_per_col, s2_per_col;
+};
+// Its leading counters must be zero before first use and are left zero by every launch.
+size_t moe_workspace_bytes(int tokens, int topk, int experts, int hidden, int inner);
+hipError_t launch_moe(MoeArgs a, int xf, int wf, int act, bool gated, void* workspace, hipStream_t st);
+
 // Weight gradient from FP8 codes.
 struct WgradArgs {
   const uint16_t* g;     // bf16 [m, n]

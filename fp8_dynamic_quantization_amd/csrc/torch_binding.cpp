@@ -483,6 +483,144 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// Router logits: [tokens, experts].
+Tensor logits_of(const Tensor& t, int* xt) {
+  *xt = real_type(t, "logits");
+  return t.contiguous();
+}
+
+// logits, topk, score, renormalize, ids, weights -> ids, weights
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 6);
+  const Tensor l0 = tensor(a[0], "logits");
+  const int64_t topk = integer(a[1]);
+  const int score = (int)integer(a[2]);
+  const bool renorm = a[3] == Py_True;
+  Tensor ids = maybe(a[4], "ids"), w = maybe(a[5], "weights");
+  hq_status st;
+  {
+    const NoGil nogil;
+    int xt;
+    const Tensor l = logits_of(l0, &xt);
+    const int64_t tokens = l.size(0), experts = l.size(1);
+    TORCH_CHECK_VALUE(topk >= 1 && topk <= 16, "topk must be in [1, 16], got ", topk);
+    const c10::OptionalDeviceGuard guard(l.device());
+    ids = output(ids, {tokens, topk}, ScalarType::Int, l, "ids");
+    w = output(w, {tokens, topk}, ScalarType::Float, l, "weights");
+    on_gpu(l, "logits");
+    st = hq_moe_route(ptr(l), xt, tokens, experts, (int)topk, score, renorm, ptr<int32_t>(ids), ptr<float>(w), stream_of(l));
+  }
+  raise_unless_ok(st);
+  return wrap_all(ids, w);
+  END_HANDLE_TH_ERRORS
+}
+
+// logits, ids, dweights, score, renormalize, dlogits -> dlogits
+PyObject* moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want(n, 6);
+  const Tensor l0 = tensor(a[0], "logits"), ids0 = tensor(a[1], "ids"), dw0 = tensor(a[2], "dweights");
+  const int score = (int)integer(a[3]);
+  const bool renorm = a[4] == Py_True;
+  Tensor dl = maybe(a[5], "dlogits");
+  hq_status st;
+  {
+    const NoGil nogil;
+    int xt;
+    const Tensor l = logits_of(l0, &xt);
+    const int64_t tokens = l.size(0), experts = l.size(1);
+    TORCH_CHECK_VALUE(ids0.dim() == 2, "ids must be 2-D [tokens, topk]");
+    const int64_t topk = ids0.size(1);
+    TORCH_CHECK_VALUE(topk >= 1 && topk <= 16, "topk must be in [1, 16], got ", topk);
+    const Tensor ids = input(ids0, {tokens, topk}, ScalarType::Int, l, "ids");
+    const Tensor dw = input(dw0, {tokens, topk}, ScalarType::Float, l, "dweights");
+    const c10::OptionalDeviceGuard guard(l.device());
+    dl = output(dl, {tokens, experts}, l.scalar_type(), l, "dlogits");
+    on_gpu(l, "logits");
+    st = hq_moe_route_backward(ptr(l), ptr<int32_t>(ids), ptr<float>(dw), xt, tokens, experts, (int)topk, score, renorm, ptr(dl),
+                               stream_of(l));
+  }
+  raise_unless_ok(st);
+  return wrap(dl);
+  END_HANDLE_TH_ERRORS
+}
+
+// The codes of an expert layer's weights, and a scale per expert [E] or per expert and row [E, rows].
+void check_expert_weight(const Tensor& codes, int64_t experts, int64_t rows, int64_t k, const Tensor& like, const char* name) {
+  TORCH_CHECK_VALUE(codes.scalar_type() == ScalarType::Byte && codes.is_contiguous() &&
+                        codes.numel() >= experts * hq_preshuffled_bytes(rows, k),
+                    name, " must hold the pre-shuffled codes of ", experts, " weights [", rows, ", ", k, "]");
+  TORCH_CHECK_VALUE(codes.device() == like.device(), name, " must be on ", like.device(), ", got ", codes.device());
+}
+Tensor expert_scale(const Tensor& t, int64_t experts, int64_t rows, const Tensor& like, const char* name) {
+  if (t.dim() == 1) return input(t, {experts}, ScalarType::Float, like, name);
+  return input(t, {experts, rows}, ScalarType::Float, like, name);
+}
+
+// xq, xf, x_scale, ids, weights, w1_pre, w1_scale, w2_pre, w2_scale, wf, inner, act, gated, bias1, bias2, residual, out,
+// workspace (None: the shared one) -> out
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  want(nargs, 18);
+  const Tensor xq0 = tensor(a[0], "xq"), xs0 = tensor(a[2], "x_scale"), ids0 = tensor(a[3], "ids"), wt0 = tensor(a[4], "weights");
+  const Tensor w1 = tensor(a[5], "w1_pre"), s10 = tensor(a[6], "w1_scale"), w2 = tensor(a[7], "w2_pre"), s20 = tensor(a[8], "w2_scale");
+  const int xf = (int)integer(a[1]), wf = (int)integer(a[9]), act = (int)integer(a[11]);
+  const int64_t inner = integer(a[10]);
+  const bool gated = a[12] == Py_True;
+  const Tensor b10 = maybe(a[13], "bias1"), b20 = maybe(a[14], "bias2"), res0 = maybe(a[15], "residual");
+  Tensor out = maybe(a[16], "out"), work = maybe(a[17], "workspace"), xq, xs, ids, wt, s1, s2, b1, b2, res;
+  int64_t tokens, hidden, topk, experts, need;
+  {
+    const NoGil nogil;
+    TORCH_CHECK_VALUE(xq0.dim() == 2 && xq0.scalar_type() == ScalarType::Byte, "xq must be uint8 codes [tokens, hidden]");
+    TORCH_CHECK_VALUE(ids0.dim() == 2, "ids must be 2-D [tokens, topk]");
+    TORCH_CHECK_VALUE(s10.dim() == 1 || s10.dim() == 2, "w1_scale must be [experts] or [experts, rows]");
+    xq = xq0.contiguous();
+    tokens = xq.size(0);
+    hidden = xq.size(1);
+    topk = ids0.size(1);
+    experts = s10.size(0);
+    TORCH_CHECK_VALUE(topk >= 1 && topk <= 16, "topk must be in [1, 16], got ", topk);
+    need = hq_moe_workspace_bytes(tokens, (int)topk, experts, hidden, inner);
+    TORCH_CHECK_VALUE(need >= 0 && (!gated || inner % 32 == 0), "tokens must be at most 64 (", tokens, "), experts in [1, 1024] (",
+                      experts, "), hidden and inner multiples of 16 (gated: inner of 32) up to 65536 (", hidden, ", ", inner, ")");
+    const int64_t n1 = gated ? 2 * inner : inner;
+    ids = input(ids0, {tokens, topk}, ScalarType::Int, xq, "ids");
+    wt = input(wt0, {tokens, topk}, ScalarType::Float, xq, "weights");
+    xs = input(xs0, xs0.sizes(), ScalarType::Float, xq, "x_scale");
+    check_expert_weight(w1, experts, n1, hidden, xq, "w1_pre");
+    check_expert_weight(w2, experts, hidden, inner, xq, "w2_pre");
+    s1 = expert_scale(s10, experts, n1, xq, "w1_scale");
+    s2 = expert_scale(s20, experts, hidden, xq, "w2_scale");
+    b1 = input(b10, {experts, n1}, ScalarType::BFloat16, xq, "bias1");
+    b2 = input(b20, {experts, hidden}, ScalarType::BFloat16, xq, "bias2");
+    res = input(res0, {tokens, hidden}, ScalarType::BFloat16, xq, "residual");
+    check_workspace(work, xq);
+    const c10::OptionalDeviceGuard guard(xq.device());
+    out = output(out, {tokens, hidden}, ScalarType::BFloat16, xq, "out");
+    on_gpu(xq, "xq");
+  }
+  const c10::OptionalDeviceGuard guard(xq.device());
+  if (!work.defined() && need > 0) {
+    THPObjectPtr dev(THPDevice_New(xq.device()));
+    THPObjectPtr r(PyObject_CallFunction(g_gemm_workspace, "OL", dev.get(), (long long)need));
+    if (!r) throw python_error();
+    work = tensor(r.get(), "workspace");
+  }
+  hq_status st;
+  {
+    const NoGil nogil;
+    const hq_moe_layer l = {ptr<uint8_t>(w1), ptr<float>(s1), s1.numel(), ptr<uint16_t>(b1), ptr<uint8_t>(w2), ptr<float>(s2),
+                            s2.numel(), ptr<uint16_t>(b2), hidden, inner, (int32_t)experts, wf, act, gated};
+    st = hq_moe_a8w8(ptr<uint8_t>(xq), xf, ptr<float>(xs), xs.numel(), ptr<int32_t>(ids), ptr<float>(wt), tokens, (int)topk, &l,
+                     ptr<uint16_t>(res), ptr<uint16_t>(out), ptr(work), bytes_of(work), stream_of(xq));
+  }
+  raise_unless_ok(st);
+  return wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // stream handle -> the number of the capture that it is part of, 0 for none
 PyObject* capture_id(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -510,7 +648,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define HQ_METHOD(F) {#F, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(F)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {HQ_METHOD(setup),        HQ_METHOD(rmsnorm_quantize), HQ_METHOD(rmsnorm_backward), HQ_METHOD(gemm_fused),
-                         HQ_METHOD(layernorm_quantize), HQ_METHOD(layernorm_backward),
+                         HQ_METHOD(layernorm_quantize), HQ_METHOD(layernorm_backward), HQ_METHOD(moe_route),
+                         HQ_METHOD(moe_route_backward), HQ_METHOD(moe),
                          HQ_METHOD(act_quantize), HQ_METHOD(act_backward),     HQ_METHOD(wgrad),            HQ_METHOD(capture_id),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hqtorch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

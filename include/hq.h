@@ -718,6 +718,101 @@ hq_status hq_wgrad_a8_strict(const uint16_t* g, const uint8_t* xq, int xf, const
                              int64_t m, int64_t n, int64_t k, const float* base, void* dw, int dwt, void* workspace,
                              size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts: the router, for any number of tokens, and the whole layer for
+ * the few tokens of a decode step, on the weights of hq_grouped_gemm_a8w8 (which
+ * serves longer batches).
+ * -------------------------------------------------------------------------- */
+
+/* How a router's logits become scores: softmax over all of a token's experts, or the
+ * logistic function of each. */
+typedef enum hq_route { HQ_ROUTE_SOFTMAX = 0, HQ_ROUTE_SIGMOID = 1 } hq_route;
+
+/* The topk experts of each token with the largest logits, in descending order (equal
+ * logits: the lower index first), and their weights:
+ *   p       = exp(l - max) / sum over all experts, or 1 / (1 + exp(-l))
+ *   weights = p, or with `renormalize` p / (sum of the chosen experts' p)
+ * An expert whose logit is -Inf or NaN is never chosen and has p = 0; slots left over
+ * get id -1 and weight 0. Logits of +Inf share the weight among themselves.
+ *   logits   device, [tokens, num_experts] of xt, row-major
+ *   score    an hq_route value; renormalize 0 or 1
+ *   ids      device, int32 [tokens, topk]
+ *   weights  device, float32 [tokens, topk]
+ * Requires 1 <= num_experts <= 1024, 1 <= topk <= min(16, num_experts), tokens <=
+ * 2^31 - 1024. Scores are float32. tokens == 0 returns HQ_OK without a launch. */
+hq_status hq_moe_route(const void* logits, int xt, int64_t tokens, int64_t num_experts, int topk, int score,
+                       int renormalize, int32_t* ids, float* weights, hipStream_t stream);
+
+/* Backward pass of the router: the gradient of sum(dweights * weights) with respect to
+ * the logits, the choice held fixed.
+ *   logits    as given to hq_moe_route
+ *   ids       device, int32 [tokens, topk]: the chosen experts. Slots whose id is not
+ *             in [0, num_experts) are left out; an expert named twice has both
+ *             slots' gradients added
+ *   dweights  device, float32 [tokens, topk]
+ *   dlogits   device, [tokens, num_experts] of xt, written in full
+ * All other arguments and the requirements are those of hq_moe_route. */
+hq_status hq_moe_route_backward(const void* logits, const int32_t* ids, const float* dweights, int xt, int64_t tokens,
+                                int64_t num_experts, int topk, int score, int renormalize, void* dlogits,
+                                hipStream_t stream);
+
+/* The weights of a mixture-of-experts layer (host struct).
+ *   w1_pre    device, num_experts consecutive pre-shuffled weights
+ *             (hq_preshuffle_weight) of [inner, hidden], gated [2 * inner, hidden]
+ *   w1_scale  device, float32 [w1_scale_count]: num_experts (one per expert) or one
+ *             per expert and row of W1
+ *   bias1     device, bf16 bits, one per expert and row of W1, or NULL
+ *   w2_pre, w2_scale, w2_scale_count, bias2
+ *             the same of [hidden, inner]
+ *   wf        format of both weights' codes
+ *   act       an hq_act value
+ *   gated     0 or 1: act(z[:inner]) * z[inner:] */
+typedef struct hq_moe_layer {
+  const uint8_t* w1_pre;
+  const float* w1_scale;
+  int64_t w1_scale_count;
+  const uint16_t* bias1;
+  const uint8_t* w2_pre;
+  const float* w2_scale;
+  int64_t w2_scale_count;
+  const uint16_t* bias2;
+  int64_t hidden, inner;
+  int32_t num_experts, wf, act, gated;
+} hq_moe_layer;
+
+/* Bytes of device workspace that hq_moe_a8w8 needs. Returns -1 for sizes that it
+ * refuses, 0 for no tokens. */
+int64_t hq_moe_workspace_bytes(int64_t tokens, int topk, int64_t num_experts, int64_t hidden, int64_t inner);
+
+/* A whole mixture-of-experts layer for at most 64 tokens, in two launches. For token t
+ * and its expert e = ids[t, j], in float32:
+ *   z      = x_scale[t] * w1_scale[e] * sum_k dec(XQ[t, k]) * dec(W1[e][:, k])  (+ bias1[e])
+ *   a      = bf16(act(z)), gated bf16(act(z[:inner]) * z[inner:])
+ *   y      = w2_scale[e] * sum_f a[f] * dec(W2[e][:, f])  (+ bias2[e])
+ *   out[t] = bf16(sum_j weights[t, j] * y  (+ residual[t]))
+ * Products are exact (16-bit matrix cores on the decoded codes). The sums are added in
+ * an order that the sizes and the ids fix: the same inputs give the same bits.
+ *   xq         device, uint8 [tokens, hidden] codes in format xf, row-major
+ *   x_scale    device, float32 [x_scale_count], x_scale_count = 1 or tokens
+ *   ids        device, int32 [tokens, topk]; a slot whose id is not in [0, num_experts)
+ *              adds nothing, whatever its weight; an expert named twice by a token
+ *              counts with the sum of both weights
+ *   weights    device, float32 [tokens, topk]
+ *   layer      host pointer
+ *   residual   device, bf16 [tokens, hidden], or NULL
+ *   out        device, bf16 [tokens, hidden]; may be the residual's own buffer
+ *   workspace  device, at least hq_moe_workspace_bytes(...) bytes. Zero-fill it once
+ *              before its first use; its first 1024 bytes are counters that every call
+ *              leaves at zero, as in the workspace of hq_gemm_a8w8, with whose calls it
+ *              may be shared. Calls that share one must not run concurrently
+ * Requires 0 <= tokens <= 64, 1 <= topk <= 16, 1 <= num_experts <= 1024, hidden and
+ * inner positive multiples of 16 (gated: inner of 32) up to 65536; 16-byte aligned xq,
+ * weights' codes, residual, out and workspace; no output may overlap an input other
+ * than as said. tokens == 0 returns HQ_OK without a launch. */
+hq_status hq_moe_a8w8(const uint8_t* xq, int xf, const float* x_scale, int64_t x_scale_count, const int32_t* ids,
+                      const float* weights, int64_t tokens, int topk, const hq_moe_layer* layer, const uint16_t* residual,
+                      uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Row-streaming probe: a measurement aid, not a step of the quantization (no
  * page defines it). It moves the bytes of a per-token quantize pass without
  * its arithmetic: for each of `rows` rows of 16-bit elements it writes the
