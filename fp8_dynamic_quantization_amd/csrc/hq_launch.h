@@ -262,7 +262,7 @@ struct MoeArgs {
   const uint16_t* b2;
   const uint16_t* residual;  // bf16 [tokens, hidden] or null
   uint16_t* out;             // bf16 [tokens, hidden]
-  uint16_t* a;               // bf16 [tokens * topk, inner], in the workspace (the launcher sets it)
+  uint16_t* a;               // activations between the kernels, in the workspace (the launcher sets it)
   int tokens, topk, experts, hidden, inner;
   int x_scale_per_row, s1_per_col, s2_per_col;
 };

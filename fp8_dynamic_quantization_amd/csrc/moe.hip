@@ -237,6 +237,7 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxPairs = kMoeMaxTokens * kMaxTopk, kMoeM
 struct MoeLds {
   int ids[kMoeMaxPairs];
   float weights[kMoeMaxPairs];
+  float x_scale[kMoeMaxTokens];
   uint32_t bits[kMoeMaxExperts / 32];
 };
 
@@ -245,6 +246,7 @@ template <int THREADS>
 __device__ __forceinline__ void moe_load_pairs(const MoeArgs& a, MoeLds& s) {
   const int pairs = a.tokens * a.topk;
   if (threadIdx.x < kMoeMaxExperts / 32) s.bits[threadIdx.x] = 0;
+  if ((int)threadIdx.x < a.tokens) s.x_scale[threadIdx.x] = a.x_scale[a.x_scale_per_row ? threadIdx.x : 0];
   __syncthreads();
   for (int p = threadIdx.x; p < pairs; p += THREADS) {
     const int e = a.ids[p];
@@ -263,19 +265,19 @@ struct ActiveExperts {
   __device__ explicit ActiveExperts(const MoeLds& s) {
     const int lane = threadIdx.x & 63;
     word = lane < 32 ? s.bits[lane] : 0u;
-    int upto = __popc(word);
-    const int own = upto;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(upto, d, 64);
-      if (lane >= d) upto += v;
-    }
+    const int own = __popc(word);
+    int upto = own;  // sums of the lanes up to this one: within a row of 16 lanes, then row 0's onto row 1
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xF, 0xF, false);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xF, 0xF, false);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xF, 0xF, false);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xF, 0xF, false);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x142, 0xA, 0xF, false);
     before = upto - own;
-    count = __builtin_amdgcn_readlane(upto, 63);
+    count = __builtin_amdgcn_readlane(upto, 31);
   }
   // The i-th of them, i < count.
   __device__ int at(int i) const {
-    const uint64_t m = __ballot(before <= i && i < before + __popc(word));
+    const uint64_t m = __ballot(before <= i && i < before + (int)__popc(word));
     const int src = __builtin_ctzll(m);
     uint32_t w = __builtin_amdgcn_readlane(word, src);
     for (int k = i - __builtin_amdgcn_readlane(before, src); k > 0; --k) w &= w - 1;
@@ -283,19 +285,28 @@ struct ActiveExperts {
   }
 };
 
-// The tokens that chose expert e, in order: their first pair with it, and the sum of
-// their weights for it (a token that names an expert twice has one row). rows and
-// wts have 64 entries of this wavefront's own.
+// A row of activations between the kernels: bf16, K blocks of 128 padded with zeros, and
+// in each block the order in which the second kernel's lanes read it. Its lane with K
+// values 32 g .. 32 g + 31 of a block loads 16 bytes at a time, so the four lanes of a row
+// find 64 contiguous bytes there (in the columns' own order they touch four times as
+// many: 64 tokens, 64 experts of 4096 x 1408, second kernel 99.6 -> 92.7 us).
+__host__ __device__ inline int moe_pitch(int inner) { return (inner + kBK - 1) / kBK * kBK; }
+__device__ __forceinline__ int moe_place(int col) { return (col & ~127) + (col >> 3 & 3) * 32 + (col >> 5 & 3) * 8 + (col & 7); }
+
+// The tokens that chose expert e, in order: their first pair with it and, where wts is
+// not null, the sum of their weights for it (a token that names an expert twice has one
+// row). rows and wts have 64 entries of this wavefront's own.
 __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s, int e, int* rows, float* wts) {
   const int t = threadIdx.x & 63;
   int p = -1;
   float w = 0.0f;
   if (t < a.tokens) {
+#pragma unroll 4
     for (int j = 0; j < a.topk; ++j) {
       const int q = t * a.topk + j;
       if (s.ids[q] == e) {
         if (p < 0) p = q;
-        w += s.weights[q];
+        if (wts) w += s.weights[q];
       }
     }
   }
@@ -303,7 +314,7 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
   if (p >= 0) {
     const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
     rows[at] = p;
-    wts[at] = w;
+    if (wts) wts[at] = w;
   }
   // LDS operations of one wavefront complete in order
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -315,131 +326,219 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // ---------------------------------------------------------------------------
 // first product and activation
 // ---------------------------------------------------------------------------
-constexpr int kMoeWaves = 8;
-
-// A workgroup owns two weight fragments of one expert: 16 columns of the first half
-// and the same columns of the second (gated), or 32 columns. Its wavefronts take the
-// K blocks w, w + 8, ..., KPW of them at a time, and meet in LDS.
-template <int XF, int WF, int MB, bool GATED>
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeArgs a, int strips, int act) {
-  constexpr int KPW = 2;
+// A unit is two weight fragments of one expert: 16 columns of the first half and the
+// same columns of the second (gated), or 32 columns. The units that the step asks for
+// are dealt over the workgroups, which fill the device once, in chunks of neighbours
+// (an expert with many rows takes longer: its units go to many workgroups). A
+// workgroup's W wavefronts take a unit's K blocks w, w + W, ... and meet in LDS at its
+// end. The next block's weights and codes, also those of the next unit's first block,
+// are on their way while one is multiplied. Loads return in order, so the codes travel
+// with the weights: fetched when needed, they would wait for all weights in flight. Only
+// an expert's rows past 16, rare, are fetched that way.
+template <int XF, int WF, int MB, bool GATED, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ? 3 : 4))) void moe_up_kernel(MoeArgs a, int strips, int chunk,
+                                                                                                   int act) {
+  // two buffers for the sums save a barrier; with more row blocks they would cost a workgroup per CU
+  constexpr int kBufs = W > 1 && MB == 1 ? 2 : 1;
   __shared__ MoeLds s;
-  __shared__ int s_rows[kMoeWaves][kMoeMaxTokens];
-  __shared__ float s_wts[kMoeWaves][kMoeMaxTokens];
-  __shared__ __attribute__((aligned(16))) v4f red[kMoeWaves][2 * MB][64];
+  __shared__ int s_rows[2][W][kMoeMaxTokens];  // of two experts in turn
+  __shared__ __attribute__((aligned(16))) v4f red[kBufs][W > 1 ? W : 1][W > 1 ? 2 * MB : 1][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = blockIdx.x / strips, strip = blockIdx.x % strips;
-  moe_load_pairs<64 * kMoeWaves>(a, s);
+  moe_load_pairs<64 * W>(a, s);
   const ActiveExperts active(s);
-  if (slot >= active.count) return;
-  const int e = active.at(slot);
-  const int nrows = moe_expert_rows(a, s, e, s_rows[wave], s_wts[wave]);
+  const int all = active.count * strips;
+  if ((int)blockIdx.x * chunk >= all) return;
 
   const int K = a.hidden, nkb = (K + kBK - 1) / kBK;
   const int n1 = GATED ? 2 * a.inner : a.inner;
-  const int frag[2] = {GATED ? strip : 2 * strip, GATED ? a.inner / 16 + strip : 2 * strip + 1};
-  const uint8_t* w = a.w1 + (size_t)e * (size_t)frag_rows(n1) * nkb * kFragBytes;
-  __amdgpu_buffer_rsrc_t w_rsrc[2];
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-    w_rsrc[f] = __builtin_amdgcn_make_buffer_rsrc((void*)(w + (size_t)frag[f] * nkb * kFragBytes), (short)0, nkb * kFragBytes,
-                                                  kRsrcFlags);
+  const size_t w_bytes = (size_t)frag_rows(n1) * nkb * kFragBytes;
   const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.xq, (short)0, a.tokens * K, kRsrcFlags);
   const int xr = lane & 15, xc = 32 * (lane >> 4);
+  auto fragment = [&](int f, int strip) { return GATED ? (f ? a.inner / 16 + strip : strip) : 2 * strip + f; };
 
-  for (int r0 = 0; r0 < nrows; r0 += 16 * MB) {
-    int xo[MB];  // byte offset of the lane's row
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int r = r0 + 16 * i + xr;
-      xo[i] = r < nrows ? s_rows[wave][r] / a.topk * K : kBadOffset;
+  struct Unit {
+    int at, slot, strip, e, rows, list;
+  };
+  __amdgpu_buffer_rsrc_t w_rsrc[2];
+  auto row_offset = [&](const Unit& u, int i) {
+    const int r = 16 * i + xr;
+    return r < u.rows ? s_rows[u.list][wave][r] / a.topk * K + xc : kBadOffset;
+  };
+  int xo;  // the lane's first row
+  auto enter = [&](Unit& u) {
+    const int slot = u.at / strips;
+    u.strip = u.at - slot * strips;
+    if (slot != u.slot) {
+      u.slot = slot;
+      u.e = active.at(slot);
+      u.list ^= 1;
+      u.rows = moe_expert_rows(a, s, u.e, s_rows[u.list][wave], nullptr);
+      xo = row_offset(u, 0);
     }
-    v4f acc[2][MB];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      w_rsrc[f] = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w1 + u.e * w_bytes + (size_t)fragment(f, u.strip) * nkb * kFragBytes),
+                                                    (short)0, nkb * kFragBytes, kRsrcFlags);
+  };
+  auto load_x = [&](uint4 (&x)[2], int off, int kb) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = kb * kBK + 16 * h;
+      x[h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, col + xc < K && off >= 0 ? off + col : kBadOffset, 0, 0));
+    }
+  };
+  struct Chunk {
+    uint4 w[2][2], x[2];
+  };
+  auto load = [&](Chunk& c, int kb) {
+    const int wo = kb < nkb ? lane * 16 : kBadOffset;  // the scalar offset is not range-checked
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int i = 0; i < MB; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int kb0 = wave; kb0 < nkb; kb0 += KPW * kMoeWaves) {
-      uint4 fb[KPW][2][2], fx[KPW][MB][2];
+      for (int h = 0; h < 2; ++h)
+        c.w[f][h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(w_rsrc[f], wo + h * 1024, min(kb, nkb - 1) * kFragBytes, kNtLoad));
+    load_x(c.x, xo, kb);
+    __builtin_amdgcn_sched_barrier(0);  // ahead of the products that follow
+  };
+
+  v4f acc[2][MB];
+  Unit cur;
+  auto multiply = [&](const Chunk& c, int kb) {
 #pragma unroll
-      for (int j = 0; j < KPW; ++j) {
-        const int kb = kb0 + j * kMoeWaves;
-        const int wo = kb < nkb ? lane * 16 : kBadOffset;  // the scalar offset is not range-checked
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            fb[j][f][h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(w_rsrc[f], wo + h * 1024, min(kb, nkb - 1) * kFragBytes, kNtLoad));
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = kb * kBK + xc + 16 * h;
-            fx[j][i][h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(x_rsrc, col < K && xo[i] >= 0 ? xo[i] + col : kBadOffset, 0, 0));
-          }
+    for (int i = 0; i < MB; ++i) {
+      uint4 late[2];
+      if (i > 0) {
+        if (16 * i >= cur.rows) break;  // wavefront-uniform
+        load_x(late, row_offset(cur, i), kb);
       }
-      __builtin_amdgcn_sched_barrier(0);  // every load of the chunk ahead of its first product
+      const uint4(&x)[2] = i > 0 ? late : c.x;
+      // 8 values of K per lane at a time: few converted codes are alive
 #pragma unroll
-      for (int j = 0; j < KPW; ++j) {
-        h8v wh[2][4];
+      for (int q = 0; q < 4; ++q) {
+        const uint4& xs = x[q >> 1];
+        const h8v xh = q & 1 ? f16x8<XF>(xs.z, xs.w) : f16x8<XF>(xs.x, xs.y);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) f16_frag<WF>(fb[j][f][0], fb[j][f][1], wh[f]);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          h8v xh[4];
-          f16_frag<XF>(fx[j][i][0], fx[j][i][1], xh);
-#pragma unroll
-          for (int f = 0; f < 2; ++f) acc[f][i] = mfma_f16x4(wh[f], xh, acc[f][i]);
+        for (int f = 0; f < 2; ++f) {
+          const uint4& ws = c.w[f][q >> 1];
+          const h8v wh = q & 1 ? f16x8<WF>(ws.z, ws.w) : f16x8<WF>(ws.x, ws.y);
+          acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh, xh, acc[f][i], 0, 0, 0);
         }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  constexpr int kParts = GATED ? MB : 2 * MB;  // 16 rows (gated), or one fragment of them
+  int parity = 0, turn = 0;
+  float sc[2][4];
+  // Scales of the lane's 4 columns of each fragment.
+  auto load_scales = [&]() {
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 2; ++f) {
+      const int nb = fragment(f, cur.strip);
+      const int col = 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1);
 #pragma unroll
-      for (int i = 0; i < MB; ++i) red[wave][f * MB + i][lane] = acc[f][i];
-    __syncthreads();
-    // Wavefront i finishes the 16 rows i (gated), wavefront 2 i + f their fragment f.
-    const int i = GATED ? wave : wave >> 1;
-    const int r = r0 + 16 * i + xr;
-    if (i < MB && r < nrows) {
-      const int pair = s_rows[wave][r];
-      const float xs = a.x_scale[a.x_scale_per_row ? pair / a.topk : 0];
+      for (int q = 0; q < 4; ++q) sc[f][q] = a.s1[a.s1_per_col ? (size_t)cur.e * n1 + min(col + q, n1 - 1) : cur.e];
+    }
+  };
+  auto finish = [&]() {
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+          if (16 * i < cur.rows) red[parity][wave][f * MB + i][lane] = acc[f][i];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      const int i = GATED ? part : part >> 1;
+      if ((W > 1 && (part + turn) % W != wave) || 16 * i >= cur.rows) continue;
+      const int r = 16 * i + xr;
+      const int pair = s_rows[cur.list][wave][min(r, cur.rows - 1)];
+      const float xs = s.x_scale[pair / a.topk];
       float z[2][4];
 #pragma unroll
       for (int f = 0; f < (GATED ? 2 : 1); ++f) {
-        const int ff = GATED ? f : wave & 1;
-        v4f t = red[0][ff * MB + i][lane];
+        const int ff = GATED ? f : part & 1;
+        v4f t;
+        if constexpr (W == 1) {
+          t = acc[ff][i];
+        } else {
+          t = red[parity][0][ff * MB + i][lane];
 #pragma unroll
-        for (int v = 1; v < kMoeWaves; ++v) t += red[v][ff * MB + i][lane];
-        const int nb = ff ? frag[1] : frag[0];
-        const int col = 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1);
+          for (int v = 1; v < W; ++v) t += red[parity][v][ff * MB + i][lane];
+        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const size_t at = (size_t)e * n1 + min(col + q, n1 - 1);
-          z[f][q] = t[q] * xs * a.s1[a.s1_per_col ? at : e];
-          if (a.b1) z[f][q] += __uint_as_float((uint32_t)a.b1[at] << 16);
+        for (int q = 0; q < 4; ++q) z[f][q] = t[q] * xs * sc[ff][q];
+        if (a.b1) {
+          const int nb = fragment(ff, cur.strip);
+          const int col = 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            z[f][q] += __uint_as_float((uint32_t)a.b1[(size_t)cur.e * n1 + min(col + q, n1 - 1)] << 16);
         }
       }
       float o[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        o[q] = z[0][q];
-      }
+      for (int q = 0; q < 4; ++q) o[q] = z[0][q];
       fused_act<4>(act, o);
       if constexpr (GATED) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] *= z[1][q];
       }
-      const int nb = GATED || !(wave & 1) ? frag[0] : frag[1];
+      const int nb = fragment(GATED ? 0 : part & 1, cur.strip);
       const int col = 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1);
-      if (col < a.inner) {
+      if (r < cur.rows) {
+        uint16_t* row = a.a + (size_t)pair * moe_pitch(a.inner);
         const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{o[0], o[1]}), bf2v));
         const uint32_t w1 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{o[2], o[3]}), bf2v));
-        *reinterpret_cast<uint2*>(a.a + (size_t)pair * a.inner + col) = make_uint2(w0, w1);
+        if (col < a.inner) *reinterpret_cast<uint2*>(row + moe_place(col)) = make_uint2(w0, w1);
+        if (cur.strip + 1 == strips)  // the row's end is zeros
+          for (int z = a.inner + 4 * (lane >> 4); z < moe_pitch(a.inner); z += 16)
+            *reinterpret_cast<uint2*>(row + moe_place(z)) = make_uint2(0u, 0u);
       }
     }
-    __syncthreads();
+    if constexpr (kBufs == 2) parity ^= 1;
+    else if constexpr (W > 1) __syncthreads();
+    turn = (turn + kParts) % W;
+  };
+
+  Unit next{(int)blockIdx.x * chunk, -1, 0, 0, 0, 0};
+  enter(next);
+  Chunk c0, c1;
+  load(c0, wave);
+  int in_chunk = 0;
+  for (;;) {
+    cur = next;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int kb = wave;; kb += 2 * W) {
+      const bool more = kb + W < nkb;
+      if (more) load(c1, kb + W);
+      if (MB == 1 && kb == wave) load_scales();  // (more row blocks have no registers for them)
+      multiply(c0, kb);
+      if (!more) break;
+      const bool again = kb + 2 * W < nkb;
+      if (again) load(c0, kb + 2 * W);
+      multiply(c1, kb + W);
+      if (!again) break;
+    }
+    if (MB > 1) load_scales();
+    if (++in_chunk == chunk) {
+      in_chunk = 0;
+      next.at += (int)(gridDim.x - 1) * chunk;
+    }
+    const bool more = ++next.at < all;
+    if (more) {
+      enter(next);
+      load(c0, wave);
+    }
+    finish();
+    if (!more) return;
   }
 }
 
@@ -464,154 +563,174 @@ __device__ __forceinline__ b8v bf16x8(uint32_t d0, uint32_t d1) {
   return b8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A workgroup owns FB weight fragments (16 FB output columns) of every expert, and all
-// tokens; the (expert, K block) pairs are dealt in runs over its wavefronts and over
-// `splits` workgroups. A wavefront adds an expert's weighted rows into sums of its own
-// in LDS ([token][column], TB tokens), so no two lanes meet; at the end the wavefronts'
-// sums are added in order, and with splits > 1 the last workgroup to arrive adds the
-// workgroups' sums, in order too: the result does not depend on who ends first.
-template <int WF, int MB, int FB, int TB>
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeArgs a, int splits, uint32_t* counters, float* partials) {
-  constexpr int KPW = 2;
-  constexpr int kCols = 16 * FB, kPitch = kCols + 4;
+// A workgroup owns one weight fragment (16 output columns) of every expert, and all
+// tokens; the (expert, K block) items are dealt in runs over its W wavefronts and over
+// `splits` workgroups. The next item's operands are on their way while one is
+// multiplied (rows past 16 as above). A wavefront adds an expert's weighted rows into
+// sums of its own in LDS ([token][column], 16 MB tokens), so no two lanes meet; at the end
+// the wavefronts' sums are added in order, and with splits > 1 the last workgroup to
+// arrive adds the workgroups' sums, in order too: the result does not depend on who ends
+// first.
+template <int WF, int MB, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void moe_down_kernel(MoeArgs a, int splits,
+                                                                                                     uint32_t* counters, float* partials) {
+  constexpr int TB = 16 * MB, kPitch = 20;
   __shared__ MoeLds s;
-  __shared__ int s_rows[kMoeWaves][kMoeMaxTokens];
-  __shared__ float s_wts[kMoeWaves][kMoeMaxTokens];
-  __shared__ __attribute__((aligned(16))) float sums[kMoeWaves][TB][kPitch];
+  __shared__ int s_rows[2][W][kMoeMaxTokens];
+  __shared__ float s_wts[2][W][kMoeMaxTokens];
+  __shared__ __attribute__((aligned(16))) float sums[W][TB][kPitch];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strip = blockIdx.x / splits, split = blockIdx.x % splits;
   for (int i = lane; i < a.tokens * (kPitch / 4); i += 64)
     *reinterpret_cast<v4f*>(&sums[wave][0][0] + 4 * i) = v4f{0.f, 0.f, 0.f, 0.f};
-  moe_load_pairs<64 * kMoeWaves>(a, s);
+  moe_load_pairs<64 * W>(a, s);
   const ActiveExperts active(s);
 
   const int K = a.inner, nkb = (K + kBK - 1) / kBK;
   const int nfrag = frag_rows(a.hidden);
-  const int nb0 = strip * FB;
   const int xr = lane & 15, xq = lane >> 4;
+  const int col0 = 32 * (strip >> 1) + 8 * xq + 4 * (strip & 1);  // the lane's 4 columns
+  // At the end a thread has 4 columns of a token; what is added to them is fetched now.
+  const int t_end = threadIdx.x >> 2, col_end = 32 * (strip >> 1) + 8 * (threadIdx.x & 3) + 4 * (strip & 1);
+  const bool ends = t_end < a.tokens && col_end < a.hidden;
+  uint2 res = make_uint2(0u, 0u);
+  if (a.residual && ends) res = *reinterpret_cast<const uint2*>(a.residual + (size_t)t_end * a.hidden + col_end);
   const __amdgpu_buffer_rsrc_t a_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc((void*)a.a, (short)0, a.tokens * a.topk * K * 2, kRsrcFlags);
+      __builtin_amdgcn_make_buffer_rsrc((void*)a.a, (short)0, a.tokens * a.topk * moe_pitch(K) * 2, kRsrcFlags);
   const int64_t items = (int64_t)active.count * nkb;
-  const int runs = splits * kMoeWaves, run = split * kMoeWaves + wave;
-  const int last = (int)(items * (run + 1) / runs);
-  for (int it = (int)(items * run / runs); it < last;) {
-    const int slot = it / nkb, kb0 = it % nkb, kb1 = min(nkb, kb0 + last - it);
-    it += kb1 - kb0;
-    const int e = active.at(slot);
-    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(a.w2 + ((size_t)e * nfrag + nb0) * nkb * kFragBytes), (short)0, FB * nkb * kFragBytes, kRsrcFlags);
-    const int nrows = moe_expert_rows(a, s, e, s_rows[wave], s_wts[wave]);
-    // the lane's 4 columns of each fragment: scales and, where the run holds the first K block, the bias
-    float sc[FB][4], bias[FB][4];
+  const int runs = splits * W, run = split * W + wave;
+  const int first = (int)(items * run / runs), last = (int)(items * (run + 1) / runs);
+
+  if (first < last) {
+    struct Segment {  // a run's items of one expert: K blocks kb0 .. kb1 - 1
+      int slot, e, rows, list, kb0, kb1;
+    };
+    __amdgpu_buffer_rsrc_t w_rsrc;
+    auto row_offset = [&](const Segment& g, int i) {  // byte offset of the lane's row and columns
+      const int r = 16 * i + xr;
+      return r < g.rows ? s_rows[g.list][wave][r] * moe_pitch(K) * 2 + 16 * xq : kBadOffset;
+    };
+    int ao;
+    auto enter = [&](Segment& g, int at) {
+      g.kb1 = min(nkb, g.kb0 + last - at);
+      g.e = active.at(g.slot);
+      g.list ^= 1;
+      g.rows = moe_expert_rows(a, s, g.e, s_rows[g.list][wave], s_wts[g.list][wave]);
+      ao = row_offset(g, 0);
+      w_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w2 + ((size_t)g.e * nfrag + strip) * nkb * kFragBytes), (short)0,
+                                                 nkb * kFragBytes, kRsrcFlags);
+    };
+    auto load_a = [&](uint4 (&v)[4], int off, int kb) {
 #pragma unroll
-    for (int f = 0; f < FB; ++f) {
-      const int nb = nb0 + f;
-      const int col = 32 * (nb >> 1) + 8 * xq + 4 * (nb & 1);
+      for (int m = 0; m < 4; ++m) v[m] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(a_rsrc, off + 64 * m, kb * 2 * kBK, 0));
+    };
+    struct Chunk {
+      uint4 w[2], v[4];
+    };
+    auto load = [&](Chunk& c, int kb) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const size_t at = (size_t)e * a.hidden + min(col + q, a.hidden - 1);
-        sc[f][q] = a.s2[a.s2_per_col ? at : e];
-        bias[f][q] = a.b2 && kb0 == 0 ? __uint_as_float((uint32_t)a.b2[at] << 16) : 0.0f;
-      }
-    }
-    for (int r0 = 0; r0 < nrows; r0 += 16 * MB) {
-      int ao[MB];  // byte offset of the lane's row
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const int r = r0 + 16 * i + xr;
-        ao[i] = r < nrows ? s_rows[wave][r] * K * 2 : kBadOffset;
-      }
-      v4f acc[FB][MB];
-#pragma unroll
-      for (int f = 0; f < FB; ++f)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) acc[f][i] = v4f{0.f, 0.f, 0.f, 0.f};
-      for (int kc = kb0; kc < kb1; kc += KPW) {
-        uint4 fb[KPW][FB][2], fa[KPW][MB][4];
-#pragma unroll
-        for (int j = 0; j < KPW; ++j) {
-          const int kb = kc + j;
-          const bool in = kb < kb1;
-#pragma unroll
-          for (int f = 0; f < FB; ++f)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              fb[j][f][h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(w_rsrc, in ? lane * 16 + h * 1024 : kBadOffset,
-                                                                           (f * nkb + min(kb, nkb - 1)) * kFragBytes, kNtLoad));
-#pragma unroll
-          for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int col = kb * kBK + 32 * xq + 8 * m;
-              fa[j][i][m] = as_uint4(
-                  __builtin_amdgcn_raw_buffer_load_b128(a_rsrc, in && col < K && ao[i] >= 0 ? ao[i] + 2 * col : kBadOffset, 0, 0));
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // every load of the chunk ahead of its first product
-#pragma unroll
-        for (int j = 0; j < KPW; ++j)
-#pragma unroll
-          for (int f = 0; f < FB; ++f) {
-            const uint4 &lo = fb[j][f][0], &hi = fb[j][f][1];
-            const b8v w[4] = {bf16x8<WF>(lo.x, lo.y), bf16x8<WF>(lo.z, lo.w), bf16x8<WF>(hi.x, hi.y), bf16x8<WF>(hi.z, hi.w)};
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[m], __builtin_bit_cast(b8v, fa[j][i][m]), acc[f][i], 0, 0, 0);
-          }
-      }
-      // lane l holds row l % 16 and 4 columns of each fragment
+      for (int h = 0; h < 2; ++h)
+        c.w[h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(w_rsrc, lane * 16 + h * 1024, kb * kFragBytes, 0));
+      load_a(c.v, ao, kb);
+      __builtin_amdgcn_sched_barrier(0);  // ahead of the products that follow
+    };
+    v4f acc[MB];
+    float sc[4];
+    Segment cur;
+    auto multiply = [&](const Chunk& c, int kb) {
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
-        const int r = r0 + 16 * i + xr;
-        if (r >= nrows) continue;
-        float* row = sums[wave][s_rows[wave][r] / a.topk];
-        const float wt = s_wts[wave][r];
+        uint4 late[4];
+        if (i > 0) {
+          if (16 * i >= cur.rows) break;  // wavefront-uniform
+          load_a(late, row_offset(cur, i), kb);
+        }
+        const uint4(&v)[4] = i > 0 ? late : c.v;
 #pragma unroll
-        for (int f = 0; f < FB; ++f) {
-          v4f* p = reinterpret_cast<v4f*>(row + 16 * f + 4 * xq);
-          v4f t = *p;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) t[q] = fmaf(wt, fmaf(acc[f][i][q], sc[f][q], bias[f][q]), t[q]);
-          *p = t;
+        for (int m = 0; m < 4; ++m) {
+          const uint4& ws = c.w[m >> 1];
+          const b8v w = m & 1 ? bf16x8<WF>(ws.z, ws.w) : bf16x8<WF>(ws.x, ws.y);
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(b8v, v[m]), acc[i], 0, 0, 0);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_scales = [&]() {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sc[q] = a.s2[a.s2_per_col ? (size_t)cur.e * a.hidden + min(col0 + q, a.hidden - 1) : cur.e];
+    };
+    Segment next{first / nkb, 0, 0, 0, 0, 0};
+    next.kb0 = first - next.slot * nkb;
+    int at = first;  // first item of the segment
+    enter(next, at);
+    Chunk c0, c1;
+    load(c0, next.kb0);
+    for (;;) {
+      cur = next;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int kb = cur.kb0;; kb += 2) {
+        const bool more = kb + 1 < cur.kb1;
+        if (more) load(c1, kb + 1);
+        if (MB == 1 && kb == cur.kb0) load_scales();  // (more row blocks have no registers for them)
+        multiply(c0, kb);
+        if (!more) break;
+        const bool again = kb + 2 < cur.kb1;
+        if (again) load(c0, kb + 2);
+        multiply(c1, kb + 1);
+        if (!again) break;
+      }
+      if (MB > 1) load_scales();
+      at += cur.kb1 - cur.kb0;
+      const bool more = at < last;
+      if (more) {
+        ++next.slot;
+        next.kb0 = 0;
+        enter(next, at);
+        load(c0, 0);
+      }
+      // lane l holds row l % 16 and 4 columns
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int r = 16 * i + xr;
+        if (r >= cur.rows) continue;
+        const float wt = s_wts[cur.list][wave][r];
+        v4f* p = reinterpret_cast<v4f*>(&sums[wave][s_rows[cur.list][wave][r] / a.topk][4 * xq]);
+        v4f t = *p;
+        const bool biased = a.b2 && cur.kb0 == 0;  // with the expert's first K block
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y = acc[i][q] * sc[q];
+          if (biased) y += __uint_as_float((uint32_t)a.b2[(size_t)cur.e * a.hidden + min(col0 + q, a.hidden - 1)] << 16);
+          t[q] = fmaf(wt, y, t[q]);
+        }
+        *p = t;
+      }
+      if (!more) break;
     }
   }
   __syncthreads();
 
-  // 4 columns of a token per thread
-  const int units = a.tokens * 4 * FB;
-  auto column = [&](int u) {
-    const int nb = nb0 + u % (4 * FB) / 4;
-    return 32 * (nb >> 1) + 8 * (u % 4) + 4 * (nb & 1);
-  };
-  auto finish = [&](int u, v4f t) {
-    const int col = column(u);
-    if (col >= a.hidden) return;
-    const size_t off = (size_t)(u / (4 * FB)) * a.hidden + col;
-    if (a.residual) {
-      const uint2 r = *reinterpret_cast<const uint2*>(a.residual + off);
-      t += v4f{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
-    }
+  auto finish = [&](v4f t) {
+    t += v4f{bf16_lo(res.x), bf16_hi(res.x), bf16_lo(res.y), bf16_hi(res.y)};
     const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{t[0], t[1]}), bf2v));
     const uint32_t w1 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{t[2], t[3]}), bf2v));
-    *reinterpret_cast<uint2*>(a.out + off) = make_uint2(w0, w1);
+    *reinterpret_cast<uint2*>(a.out + (size_t)t_end * a.hidden + col_end) = make_uint2(w0, w1);
   };
-  float* mine = partials + ((size_t)strip * splits + split) * a.tokens * kCols;
-  for (int u = threadIdx.x; u < units; u += 64 * kMoeWaves) {
-    const int t = u / (4 * FB), c = 4 * (u % (4 * FB));
-    v4f v = *reinterpret_cast<const v4f*>(&sums[0][t][c]);
+  const size_t part = (size_t)a.tokens * 16;  // floats of a workgroup's sums
+  float* base = partials + (size_t)strip * splits * part + 4 * threadIdx.x;
+  if (ends) {
+    const float* p = &sums[0][t_end][4 * (threadIdx.x & 3)];
+    v4f v = *reinterpret_cast<const v4f*>(p);
 #pragma unroll
-    for (int w = 1; w < kMoeWaves; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][t][c]);
+    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const v4f*>(p + w * TB * kPitch);
     if (splits == 1) {
-      finish(u, v);
+      finish(v);
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) __hip_atomic_store(mine + 4 * u + q, v[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int q = 0; q < 4; ++q) __hip_atomic_store(base + split * part + q, v[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
   if (splits == 1) return;
@@ -625,15 +744,21 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeArgs a, int
     s_last = __hip_atomic_fetch_add(counters + strip, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(splits - 1);
   __syncthreads();
   if (!s_last) return;
-  const float* base = partials + (size_t)strip * splits * a.tokens * kCols;
-  for (int u = threadIdx.x; u < units; u += 64 * kMoeWaves) {
+  if (ends) {
     v4f t = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int sp = 0; sp < splits; ++sp) {
-      const float* p = base + (size_t)sp * a.tokens * kCols + 4 * u;
+    for (int s0 = 0; s0 < splits; s0 += 8) {  // 8 loads in flight; added in order
+      v4f v[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) t[q] += __hip_atomic_load(p + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int i = 0; i < 8; ++i) {
+        const float* p = base + min(s0 + i, splits - 1) * part;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[i][q] = __hip_atomic_load(p + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < splits) t += v[i];
     }
-    finish(u, t);
+    finish(t);
   }
   if (threadIdx.x == 0) __hip_atomic_store(counters + strip, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -643,57 +768,79 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeArgs a, int
 // ---------------------------------------------------------------------------
 constexpr int kMoeCounters = 256;
 
+// The second kernel's workgroups: `strips` fragments times `splits`, of `waves`
+// wavefronts; 16 wavefronts per CU where the items suffice for two each.
 struct MoePlan {
-  int fb, strips, splits;
+  int strips, splits, waves;
   size_t a_bytes, bytes;
 };
 static MoePlan moe_plan(int tokens, int topk, int experts, int hidden, int inner) {
   MoePlan p{};
-  const int nfrag = frag_rows(hidden), pairs = tokens * topk;
-  p.fb = nfrag > 2 * kNumCUs ? 2 : 1;
-  p.strips = nfrag / p.fb;
+  const int pairs = tokens * topk;
+  p.strips = frag_rows(hidden);
+  p.waves = p.strips > kNumCUs ? 8 : 16;
   p.splits = 1;
-  if (p.strips <= kMoeCounters) {
+  if (p.strips < kNumCUs) {
     const int64_t items = (int64_t)std::min(experts, pairs) * ((inner + kBK - 1) / kBK);
-    const int64_t worth = std::max<int64_t>(1, items / (2 * kMoeWaves));
-    p.splits = (int)std::min<int64_t>((2 * kNumCUs + p.strips - 1) / p.strips, worth);
+    const int64_t worth = std::max<int64_t>(1, items / (2 * p.waves));
+    p.splits = (int)std::min<int64_t>((kNumCUs + p.strips - 1) / p.strips, worth);
   }
-  p.a_bytes = ((size_t)pairs * inner * 2 + 255) / 256 * 256;
-  p.bytes = kMoeCounters * 4 + p.a_bytes +
-            (p.splits > 1 ? (size_t)p.strips * p.splits * tokens * 16 * p.fb * sizeof(float) : 0);
+  p.a_bytes = (size_t)pairs * moe_pitch(inner) * 2;
+  p.bytes = kMoeCounters * 4 + p.a_bytes + (p.splits > 1 ? (size_t)p.strips * p.splits * tokens * 16 * sizeof(float) : 0);
   return p;
 }
 size_t moe_workspace_bytes(int tokens, int topk, int experts, int hidden, int inner) {
   return moe_plan(tokens, topk, experts, hidden, inner).bytes;
 }
 
+template <int XF, int WF, int MB, int W>
+static hipError_t launch_moe_up_w(const MoeArgs& a, int act, bool gated, int strips, int units, hipStream_t st) {
+  constexpr int kResident = (MB > 1 ? 12 : 16) * kNumCUs / W;  // workgroups that the registers hold at once
+  const int groups = std::min(units, kResident);
+  const int chunk = std::max(1, units / (4 * groups));
+  if (gated) hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, true, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, chunk, act);
+  else hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, false, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, chunk, act);
+  return hipGetLastError();
+}
+
+// Wavefronts per unit: enough K blocks for two or more each, and enough wavefronts for the
+// device where units are few. Measured (us, 1 / 2 / 4 / 8; before the last steps above): 16 of
+// 128 experts 512 x 512 8.5 / 8.4 / 9.2 / 37; 40 tokens, 100 experts 256 x 2048 16.0 / 28.5 /
+// 39.9 / 140; 64 tokens, 8 experts 2048 x 2048 28.6 / 28.0 / 19.6 / 28.1; 1 token, 32 experts
+// 7168 x 768 (192 units) 29.2 / 18.3 / 13.1 / 10.4; 1 token, 64 experts 4096 x 1408 (704
+// units) 23.6 / 18.2 / 18.0 / 24.3.
 template <int XF, int WF, int MB>
 static hipError_t launch_moe_up(const MoeArgs& a, int act, bool gated, hipStream_t st) {
   const int strips = gated ? a.inner / 16 : (a.inner + 31) / 32;
-  const dim3 grid(std::min(a.experts, a.tokens * a.topk) * strips), block(64 * kMoeWaves);
-  if (gated) hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, true>), grid, block, 0, st, a, strips, act);
-  else hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, false>), grid, block, 0, st, a, strips, act);
-  return hipGetLastError();
+  const int units = std::min(a.experts, a.tokens * a.topk) * strips;
+  const int nkb = (a.hidden + kBK - 1) / kBK;
+  if (nkb <= 2) return launch_moe_up_w<XF, WF, MB, 1>(a, act, gated, strips, units, st);
+  if (nkb <= 4) return launch_moe_up_w<XF, WF, MB, 2>(a, act, gated, strips, units, st);
+  if (units >= 2 * kNumCUs || nkb <= 8) return launch_moe_up_w<XF, WF, MB, 4>(a, act, gated, strips, units, st);
+  return launch_moe_up_w<XF, WF, MB, 8>(a, act, gated, strips, units, st);
 }
 
-template <int WF, int MB, int TB>
+template <int WF, int MB>
 static hipError_t launch_moe_down(const MoeArgs& a, const MoePlan& p, uint32_t* counters, float* partials, hipStream_t st) {
-  const dim3 grid(p.strips * p.splits), block(64 * kMoeWaves);
-  if (p.fb == 1) hipLaunchKernelGGL((moe_down_kernel<WF, MB, 1, TB>), grid, block, 0, st, a, p.splits, counters, partials);
-  else hipLaunchKernelGGL((moe_down_kernel<WF, MB, 2, TB>), grid, block, 0, st, a, p.splits, counters, partials);
+  const dim3 grid(p.strips * p.splits), block(64 * p.waves);
+  if (p.waves == 8) hipLaunchKernelGGL((moe_down_kernel<WF, MB, 8>), grid, block, 0, st, a, p.splits, counters, partials);
+  else hipLaunchKernelGGL((moe_down_kernel<WF, MB, 16>), grid, block, 0, st, a, p.splits, counters, partials);
   return hipGetLastError();
 }
 
+// Row blocks of 16 that a kernel holds: as many as the step has tokens.
+template <int XF, int WF, int MB>
+static hipError_t launch_moe_m(const MoeArgs& a, int act, bool gated, const MoePlan& p, uint32_t* counters, float* partials,
+                               hipStream_t st) {
+  const hipError_t e = launch_moe_up<XF, WF, MB>(a, act, gated, st);
+  return e != hipSuccess ? e : launch_moe_down<WF, MB>(a, p, counters, partials, st);
+}
 template <int XF, int WF>
 static hipError_t launch_moe_t(const MoeArgs& a, int act, bool gated, const MoePlan& p, uint32_t* counters, float* partials,
                                hipStream_t st) {
-  // 16 rows of an expert at a time, or 32 where experts have more than 8 on average
-  const bool wide = a.tokens > 16 && a.tokens * a.topk > 8 * a.experts;
-  const hipError_t e = wide ? launch_moe_up<XF, WF, 2>(a, act, gated, st) : launch_moe_up<XF, WF, 1>(a, act, gated, st);
-  if (e != hipSuccess) return e;
-  if (a.tokens <= 16) return launch_moe_down<WF, 1, 16>(a, p, counters, partials, st);
-  if (!wide) return launch_moe_down<WF, 1, 64>(a, p, counters, partials, st);
-  return launch_moe_down<WF, 2, 64>(a, p, counters, partials, st);
+  if (a.tokens <= 16) return launch_moe_m<XF, WF, 1>(a, act, gated, p, counters, partials, st);
+  if (a.tokens <= 32) return launch_moe_m<XF, WF, 2>(a, act, gated, p, counters, partials, st);
+  return launch_moe_m<XF, WF, 4>(a, act, gated, p, counters, partials, st);
 }
 
 hipError_t launch_moe(MoeArgs a, int xf, int wf, int act, bool gated, void* workspace, hipStream_t st) {
