@@ -229,7 +229,10 @@ def _check_exact(out, ref):
 LAYERS = [(1, 1, 1, 16, 16, False), (1, 8, 2, 1024, 1024, True), (64, 1, 1, 48, 32, True), (64, 5, 2, 272, 96, True), (17, 40, 8, 256, 160, True),
           (64, 300, 16, 64, 32, True), (33, 3, 3, 2064, 368, False), (16, 16, 8, 32, 2048, True), (5, 9, 4, 144, 48, False),
           (3, 2, 1, 8208, 64, True), (40, 3, 2, 8240, 48, False), (64, 64, 8, 384, 256, True), (20, 4, 16, 400, 80, False),
-          (50, 1000, 2, 32, 16, False), (2, 3, 2, 16, 4112, False)]
+          (50, 1000, 2, 32, 16, False), (2, 3, 2, 16, 4112, False),
+          # the first kernel's wavefronts per unit with each count of row blocks, and several chunks of units per workgroup
+          (2, 3, 2, 320, 48, False), (20, 3, 2, 1168, 96, True), (24, 6, 3, 912, 64, False), (48, 4, 2, 640, 96, True),
+          (30, 40, 4, 1200, 512, True), (64, 400, 16, 16, 1024, True)]
 
 
 @pytest.mark.parametrize("tokens,experts,topk,hidden,inner,gated", LAYERS)
