@@ -285,31 +285,40 @@ struct ActiveExperts {
   }
 };
 
-// A row of activations between the kernels: bf16, K blocks of 128 padded with zeros, and
-// in each block the order in which the second kernel's lanes read it. Its lane with K
-// values 32 g .. 32 g + 31 of a block loads 16 bytes at a time, so the four lanes of a row
-// find 64 contiguous bytes there (in the columns' own order they touch four times as
-// many: 64 tokens, 64 experts of 4096 x 1408, second kernel 99.6 -> 92.7 us).
+// Activations between the kernels: bf16, the rows of an expert together, experts in
+// order, K blocks of 128 padded with zeros. An expert's rows come in blocks of 16 (n in
+// the last), a block's K blocks one after another, and in these the order in which the
+// second kernel's lanes read: its lane of row r that has K values 32 g .. 32 g + 31 loads
+// 16 bytes at a time, the m-th at ((4 m + g) n + r) 16, so that one load of a wavefront
+// reads 64 n contiguous bytes (64 tokens, 64 experts of 4096 x 1408: second kernel 82.7 us;
+// 92.4 with each pair's row by itself in that order, 99.6 with its columns in their own).
 __host__ __device__ inline int moe_pitch(int inner) { return (inner + kBK - 1) / kBK * kBK; }
-__device__ __forceinline__ int moe_place(int col) { return (col & ~127) + (col >> 3 & 3) * 32 + (col >> 5 & 3) * 8 + (col & 7); }
+// Element of column col in row r of a block of n rows, from the block's start.
+__device__ __forceinline__ int moe_place(int n, int r, int col) {
+  return ((col >> 7) * 16 + (col >> 3 & 3) * 4 + (col >> 5 & 3)) * n * 8 + r * 8 + (col & 7);
+}
 
 // The tokens that chose expert e, in order: their first pair with it and, where wts is
 // not null, the sum of their weights for it (a token that names an expert twice has one
-// row). rows and wts have 64 entries of this wavefront's own.
-__device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s, int e, int* rows, float* wts) {
+// row). rows and wts have 64 entries of this wavefront's own; before: the pairs that chose
+// an expert below e, where the expert's rows of activations start.
+__device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s, int e, int* rows, float* wts, int& before) {
   const int t = threadIdx.x & 63;
-  int p = -1;
+  int p = -1, below = 0;
   float w = 0.0f;
-  if (t < a.tokens) {
-#pragma unroll 4
-    for (int j = 0; j < a.topk; ++j) {
+  for (int j0 = 0; j0 < a.topk; j0 += 4) {
+#pragma unroll
+    for (int j = j0; j < j0 + 4; ++j) {
       const int q = t * a.topk + j;
-      if (s.ids[q] == e) {
+      const int id = t < a.tokens && j < a.topk ? s.ids[q] : -1;
+      below += __popcll(__ballot((unsigned)id < (unsigned)e));
+      if (id == e) {
         if (p < 0) p = q;
         if (wts) w += s.weights[q];
       }
     }
   }
+  before = below;
   const uint64_t m = __ballot(p >= 0);
   if (p >= 0) {
     const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
@@ -358,7 +367,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
   auto fragment = [&](int f, int strip) { return GATED ? (f ? a.inner / 16 + strip : strip) : 2 * strip + f; };
 
   struct Unit {
-    int at, slot, strip, e, rows, list;
+    int at, slot, strip, e, rows, list, before;
   };
   __amdgpu_buffer_rsrc_t w_rsrc[2];
   auto row_offset = [&](const Unit& u, int i) {
@@ -373,7 +382,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
       u.slot = slot;
       u.e = active.at(slot);
       u.list ^= 1;
-      u.rows = moe_expert_rows(a, s, u.e, s_rows[u.list][wave], nullptr);
+      u.rows = moe_expert_rows(a, s, u.e, s_rows[u.list][wave], nullptr, u.before);
       xo = row_offset(u, 0);
     }
 #pragma unroll
@@ -491,13 +500,14 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
       const int nb = fragment(GATED ? 0 : part & 1, cur.strip);
       const int col = 32 * (nb >> 1) + 8 * (lane >> 4) + 4 * (nb & 1);
       if (r < cur.rows) {
-        uint16_t* row = a.a + (size_t)pair * moe_pitch(a.inner);
+        const int n = min(16, cur.rows - 16 * i);
+        uint16_t* block = a.a + (size_t)(cur.before + 16 * i) * moe_pitch(a.inner);
         const uint32_t w0 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{o[0], o[1]}), bf2v));
         const uint32_t w1 = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{o[2], o[3]}), bf2v));
-        if (col < a.inner) *reinterpret_cast<uint2*>(row + moe_place(col)) = make_uint2(w0, w1);
+        if (col < a.inner) *reinterpret_cast<uint2*>(block + moe_place(n, xr, col)) = make_uint2(w0, w1);
         if (cur.strip + 1 == strips)  // the row's end is zeros
           for (int z = a.inner + 4 * (lane >> 4); z < moe_pitch(a.inner); z += 16)
-            *reinterpret_cast<uint2*>(row + moe_place(z)) = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(block + moe_place(n, xr, z)) = make_uint2(0u, 0u);
       }
     }
     if constexpr (kBufs == 2) parity ^= 1;
@@ -505,7 +515,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
     turn = (turn + kParts) % W;
   };
 
-  Unit next{(int)blockIdx.x * chunk, -1, 0, 0, 0, 0};
+  Unit next{(int)blockIdx.x * chunk, -1, 0, 0, 0, 0, 0};
   enter(next);
   Chunk c0, c1;
   load(c0, wave);
@@ -605,26 +615,30 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 
   if (first < last) {
     struct Segment {  // a run's items of one expert: K blocks kb0 .. kb1 - 1
-      int slot, e, rows, list, kb0, kb1;
+      int slot, e, rows, list, before, kb0, kb1;
     };
     __amdgpu_buffer_rsrc_t w_rsrc;
-    auto row_offset = [&](const Segment& g, int i) {  // byte offset of the lane's row and columns
-      const int r = 16 * i + xr;
-      return r < g.rows ? s_rows[g.list][wave][r] * moe_pitch(K) * 2 + 16 * xq : kBadOffset;
+    struct Rows {  // a block of rows: the lane's place in a K block, the first of these, their size
+      int lane_at, at, size;
     };
-    int ao;
+    auto block_rows = [&](const Segment& g, int i) {
+      const int n = min(16, g.rows - 16 * i);
+      return Rows{xr < n ? (xq * n + xr) * 16 : kBadOffset, (g.before + 16 * i) * moe_pitch(K) * 2, n * 2 * kBK};
+    };
+    Rows ao;
     auto enter = [&](Segment& g, int at) {
       g.kb1 = min(nkb, g.kb0 + last - at);
       g.e = active.at(g.slot);
       g.list ^= 1;
-      g.rows = moe_expert_rows(a, s, g.e, s_rows[g.list][wave], s_wts[g.list][wave]);
-      ao = row_offset(g, 0);
+      g.rows = moe_expert_rows(a, s, g.e, s_rows[g.list][wave], s_wts[g.list][wave], g.before);
+      ao = block_rows(g, 0);
       w_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w2 + ((size_t)g.e * nfrag + strip) * nkb * kFragBytes), (short)0,
                                                  nkb * kFragBytes, kRsrcFlags);
     };
-    auto load_a = [&](uint4 (&v)[4], int off, int kb) {
+    auto load_a = [&](uint4 (&v)[4], const Rows& b, int kb) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) v[m] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(a_rsrc, off + 64 * m, kb * 2 * kBK, 0));
+      for (int m = 0; m < 4; ++m)
+        v[m] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(a_rsrc, b.lane_at, b.at + kb * b.size + m * (b.size >> 2), 0));
     };
     struct Chunk {
       uint4 w[2], v[4];
@@ -645,7 +659,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
         uint4 late[4];
         if (i > 0) {
           if (16 * i >= cur.rows) break;  // wavefront-uniform
-          load_a(late, row_offset(cur, i), kb);
+          load_a(late, block_rows(cur, i), kb);
         }
         const uint4(&v)[4] = i > 0 ? late : c.v;
 #pragma unroll
@@ -661,7 +675,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 #pragma unroll
       for (int q = 0; q < 4; ++q) sc[q] = a.s2[a.s2_per_col ? (size_t)cur.e * a.hidden + min(col0 + q, a.hidden - 1) : cur.e];
     };
-    Segment next{first / nkb, 0, 0, 0, 0, 0};
+    Segment next{first / nkb, 0, 0, 0, 0, 0, 0};
     next.kb0 = first - next.slot * nkb;
     int at = first;  // first item of the segment
     enter(next, at);
