@@ -18,15 +18,19 @@ namespace hq {
 // row of lanes, or 64) that hold V of its logits each: lane l has experts l, l + G,
 // ... The k-th largest is found k times over: the lanes' maxima, then the lowest
 // index that holds the maximum, which leaves the race. All in registers: one read of
-// the logits.
+// the logits. Up to some thousand tokens a call takes what a launch and the rounds'
+// dependent lane moves take (1 token, 128 experts, topk 8: 3.6 us in a graph, bf16 3.0);
+// beyond, the rounds' vector instructions bound it, not the 9.4 MB: 16384 tokens, 128
+// experts, topk 8, float32 6.2 us, bf16, whose keys hold the index, 5.2 (7.0 both with
+// floats compared).
 constexpr int kMaxTopk = 16;
 
 template <int G, class F>
 __device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // swap neighbours
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // swap pairs
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // half-row mirror
-  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // swap neighbours
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // swap pairs
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));  // half-row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // row mirror
   if constexpr (G == 64) {
     v = f(v, (uint32_t)__shfl_xor((int)v, 16, 64));
     v = f(v, (uint32_t)__shfl_xor((int)v, 32, 64));
@@ -46,8 +50,12 @@ __device__ __forceinline__ float group_sum(float v) {
   }));
 }
 template <int G>
-__device__ __forceinline__ int group_min(int v) {
-  return (int)group_reduce<G>((uint32_t)v, [](uint32_t a, uint32_t b) { return min(a, b); });
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
 
 // A logit; NaN counts as -Inf.
@@ -55,6 +63,21 @@ template <int XT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   const float v = XT == kF32 ? static_cast<const float*>(p)[i] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
   return v == v ? v : -__builtin_inff();
+}
+// A logit in the race: an unsigned integer in the logits' order (negative values' bits
+// inverted, the others' sign bit set; -0 as 0), 0 for -Inf. A 16-bit logit leaves room for
+// the expert below its bits, the lowest as the largest.
+template <int XT>
+__device__ __forceinline__ uint32_t race_key(float v, int e) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  const uint32_t k = b >> 31 ? ~b : b | 0x80000000u;
+  return v == -__builtin_inff() ? 0u : XT == kF32 ? k : (k & 0xffff0000u) | (0xffffu - e);
+}
+template <int XT>
+__device__ __forceinline__ float race_logit(uint32_t k) {
+  if (k == 0) return -__builtin_inff();
+  const uint32_t b = k >> 31 ? k & 0x7fffffffu : ~k;
+  return __uint_as_float(XT == kF32 ? b : b & 0xffff0000u);
 }
 // exp(l - m) for l <= m; equal infinities differ by nothing.
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
@@ -85,10 +108,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
       const int e = l + G * j;
       v[j] = e < a.experts ? load_logit<XT>(a.logits, row * a.experts + e) : -__builtin_inff();
     }
-    float top = v[0];
+    uint32_t key[V], m = 0;
 #pragma unroll
-    for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
-    top = group_max<G>(top);
+    for (int j = 0; j < V; ++j) {
+      key[j] = race_key<XT>(v[j], l + G * j);
+      m = max(m, key[j]);
+    }
+    m = group_max<G>(m);
+    const float top = race_logit<XT>(m);
     float all = 0.0f;  // sum of the exponentials of all experts
     if (a.score == kRouteSoftmax && !a.renormalize) {
 #pragma unroll
@@ -97,25 +124,29 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
     }
     // slot r stays with lane r
     int id = -1;
-    float mine = 0.0f, m = top;
+    uint32_t won = 0;
     for (int r = 0; r < a.topk; ++r) {
-      int at = 0x7fffffff;
+      uint32_t at = 0xffffu - (m & 0xffffu);
+      if constexpr (XT == kF32) {
+        at = 0x7fffffff;
 #pragma unroll
-      for (int j = V - 1; j >= 0; --j) at = v[j] == m ? l + G * j : at;
-      at = group_min<G>(at);
-      const bool found = m != -__builtin_inff();
-      if (l == r && found) {
-        id = at;
-        mine = m;
+        for (int j = V - 1; j >= 0; --j) at = key[j] == m ? l + G * j : at;
+        at = group_min<G>(at);
       }
-      m = -__builtin_inff();
+      if (l == r && m != 0) {
+        id = at;
+        won = m;
+      }
+      const uint32_t best = m;
+      m = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (found && at == l + G * j) v[j] = -__builtin_inff();
-        m = fmaxf(m, v[j]);
+        if (XT == kF32 ? at == (uint32_t)(l + G * j) : key[j] == best) key[j] = 0;
+        m = max(m, key[j]);
       }
       m = group_max<G>(m);
     }
+    const float mine = race_logit<XT>(won);
     float w = 0.0f;
     if (a.renormalize) w = renormalised<G>(mine, id >= 0, a.score);
     else if (id >= 0) w = a.score == kRouteSigmoid ? sigmoid(mine) : exp_below(mine, top) / all;
@@ -207,13 +238,21 @@ constexpr int64_t kMaxRouteBlocks = 1 << 20;
                        0, st, a);                                                                                       \
     return hipGetLastError();                                                                                           \
   } while (0)
-#define HQ_ROUTE_X(KERNEL, XT)                           \
-  do {                                                   \
-    if (a.experts <= 64) HQ_ROUTE(KERNEL, XT, 16, 4);    \
-    if (a.experts <= 128) HQ_ROUTE(KERNEL, XT, 16, 8);   \
-    if (a.experts <= 256) HQ_ROUTE(KERNEL, XT, 16, 16);  \
-    if (a.experts <= 512) HQ_ROUTE(KERNEL, XT, 64, 8);   \
-    HQ_ROUTE(KERNEL, XT, 64, 16);                        \
+// Lanes per token, measured with topk 8, float32 (us, 16 / 64 lanes): with enough tokens
+// for every SIMD the instructions per token count, 16384 tokens 6.2 / 11.2 (128 experts),
+// 9.2 / 12.9 (256), 17.4 / 19.4 (512), 60.7 / 36.9 (1024); with fewer the length of a
+// round, 1 token 3.8 / 3.6 (128), 5.4 / 4.0 (256), 9.3 / 5.0 (512), and 64 of 64 experts
+// 3.1 / 3.8, where a lane has one logit.
+#define HQ_ROUTE_X(KERNEL, XT)                                  \
+  do {                                                          \
+    const bool few = a.tokens <= 4 * kNumCUs;                   \
+    if (a.experts <= 64) HQ_ROUTE(KERNEL, XT, 16, 4);           \
+    if (a.experts <= 128 && few) HQ_ROUTE(KERNEL, XT, 64, 2);   \
+    if (a.experts <= 128) HQ_ROUTE(KERNEL, XT, 16, 8);          \
+    if (a.experts <= 256 && few) HQ_ROUTE(KERNEL, XT, 64, 4);   \
+    if (a.experts <= 256) HQ_ROUTE(KERNEL, XT, 16, 16);         \
+    if (a.experts <= 512) HQ_ROUTE(KERNEL, XT, 64, 8);          \
+    HQ_ROUTE(KERNEL, XT, 64, 16);                               \
   } while (0)
 
 hipError_t launch_moe_route(const RouteArgs& a, int xt, hipStream_t st) {

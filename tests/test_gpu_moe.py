@@ -53,7 +53,8 @@ def _factor(values):
 
 
 # every form (64, 128, 256, 512 and 1024 experts), odd counts, one token to more than a launch's lanes hold
-ROUTES = [(1, 1, 1), (1, 128, 8), (3, 5, 5), (130, 64, 4), (17, 65, 16), (9, 200, 8), (5, 257, 3), (66, 512, 10), (4, 1000, 16), (2, 1024, 1)]
+ROUTES = [(1, 1, 1), (1, 128, 8), (3, 5, 5), (130, 64, 4), (17, 65, 16), (9, 200, 8), (5, 257, 3), (66, 512, 10), (4, 1000, 16), (2, 1024, 1),
+          (1025, 128, 8), (1030, 65, 16), (1024, 256, 3), (1037, 250, 7)]
 
 
 @pytest.mark.parametrize("tokens,experts,topk", ROUTES)
@@ -118,6 +119,38 @@ def test_route_special_logits(hq, experts, score, renorm):
     rows = [0, 1, 2, 3, 4, 6, 7, 8]
     assert np.all(np.abs(got[rows] - ref[rows]) <= (16 * 1004 + 128) * U * terms[rows] + 2.0 ** -126)
     assert not np.isnan(got).any()
+
+
+@pytest.mark.parametrize("experts", [7, 64, 100, 256, 300, 1024])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [8, 1032])
+def test_route_special_logits_each_form(hq, experts, xt, tokens):
+    """The same of both types and of few and many tokens: ids as the oracle's, equal rows alike."""
+    v = np.random.default_rng(8).standard_normal((8, experts)).astype(np.float32)
+    v[0] = 1.25
+    v[1] = -np.inf
+    v[1, [experts - 1, 3]] = [0.5, -0.25]
+    v[2] = np.nan
+    v[2, 1:4] = -np.inf
+    v[3, ::2] = np.nan
+    v[4] = -np.abs(v[4])
+    v[4, [1, 4]] = np.inf
+    v[5] = -0.0
+    v[5, 1::2] = 0.0
+    v[6] -= 1000.0
+    v[7] = float(torch.finfo(torch.bfloat16).min)
+    v[7, 4] = -3.0
+    v = np.tile(v, (tokens // 8, 1))
+    if xt == "f32":
+        l = dev_f32(v)
+    else:
+        bits = workloads.to_bf16_bits(v)
+        l, v = dev_bf16(bits), workloads.bf16_bits_to_f32(bits)
+    ids, w = hq.hq_moe_route(l, 5)
+    ids_ref, w_ref = M.route(v[:8], 5, M.SOFTMAX, True)
+    assert np.array_equal(host(ids), np.tile(ids_ref, (tokens // 8, 1)))
+    tol = (16 * (1000 + 4) + 128) * U * w_ref + 2.0 ** -126
+    assert np.all(np.abs(_f64(w) - np.tile(w_ref, (tokens // 8, 1))) <= np.tile(tol, (tokens // 8, 1)))
 
 
 def test_route_backward_ids(hq):
