@@ -382,7 +382,12 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // end. The next block's weights and codes, also those of the next unit's first block,
 // are on their way while one is multiplied. Loads return in order, so the codes travel
 // with the weights: fetched when needed, they would wait for all weights in flight. Only
-// an expert's rows past 16, rare, are fetched that way.
+// an expert's rows past 16, rare, are fetched that way. Codes are multiplied as f16, which
+// holds each of them, so every product is exact and the sums are float32.
+// Bound by the weights of the experts that are asked for, each read once and past the
+// caches' own order (non-temporal: 117 us, else 130). 64 tokens, 64 experts of 4096 x 1408,
+// 58 asked for, 669 MB: 117 us, 5.7 TB/s; 1 token, 8 of them, 92 MB: 18 us, 5.1 TB/s. Below
+// some 10 MB a launch, the pairs and one trip to memory: 5 to 6 us.
 template <int XF, int WF, int MB, bool GATED, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ? 3 : 4))) void moe_up_kernel(MoeArgs a, int strips, int chunk,
                                                                                                    int act) {
@@ -620,6 +625,15 @@ __device__ __forceinline__ b8v bf16x8(uint32_t d0, uint32_t d1) {
 // the wavefronts' sums are added in order, and with splits > 1 the last workgroup to
 // arrive adds the workgroups' sums, in order too: the result does not depend on who ends
 // first.
+// The activations are bf16, as is this product: float32's range (a gated activation passes
+// what f16 holds) in half the bytes, at half a step, 2^-8, of each term. Error against 64
+// bits, relative to the result's norm: 0.0023 with it, 0.0017 (the output's own rounding)
+// with float32 activations. Sums are float32.
+// Bound by the weights up to 16 tokens (56 of the 64 experts above, 323 MB: 53 us, 6.1 TB/s;
+// 1 token, 46 MB: 10.6 us). With more rows per expert the activations, which every
+// workgroup reads from L2, reach the weights' bytes: 64 tokens, 335 MB of weights and 380 of
+// activations, 82 us. Two fragments per item halve them, 75 us there, but leave 8
+// wavefronts per CU: 7168 x 768 35 -> 50 us, 256 x 2048 19 -> 29.
 template <int WF, int MB, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void moe_down_kernel(MoeArgs a, int splits,
                                                                                                      uint32_t* counters, float* partials) {
