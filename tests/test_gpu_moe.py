@@ -265,7 +265,9 @@ LAYERS = [(1, 1, 1, 16, 16, False), (1, 8, 2, 1024, 1024, True), (64, 1, 1, 48, 
           (50, 1000, 2, 32, 16, False), (2, 3, 2, 16, 4112, False),
           # the first kernel's wavefronts per unit with each count of row blocks, and several chunks of units per workgroup
           (2, 3, 2, 320, 48, False), (20, 3, 2, 1168, 96, True), (24, 6, 3, 912, 64, False), (48, 4, 2, 640, 96, True),
-          (30, 40, 4, 1200, 512, True), (64, 400, 16, 16, 1024, True)]
+          (30, 40, 4, 1200, 512, True), (64, 400, 16, 16, 1024, True),
+          # the largest widths
+          (3, 2, 2, 65536, 32, True), (33, 2, 1, 16, 65536, False)]
 
 
 @pytest.mark.parametrize("tokens,experts,topk,hidden,inner,gated", LAYERS)
@@ -397,6 +399,31 @@ def test_layer_strided_scalar_scale_and_other_stream(hq):
     other = hq.hq_moe_a8w8(*args, **layer.dev, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(other, out)
+
+
+def test_layer_of_many_wide_experts(hq):
+    """Weights past 4 GiB: the same bits as a layer of the chosen experts alone. The others hold NaN codes."""
+    experts, hidden, inner = 1000, 4096, 1024
+    rng = np.random.default_rng(11)
+    small = _exact_layer(hq, rng, 4, hidden, inner, True, bias=False)
+    codes, xs, v = _exact_tokens(rng, 1, hidden)
+    chosen = torch.tensor([3, 521, 640, 999], device="cuda")
+    dev = dict(small.dev)
+    for name, rows, k in (("w1", 2 * inner, hidden), ("w2", hidden, inner)):
+        big = torch.full((experts, hq.hq_preshuffled_bytes(rows, k)), 0x7F, dtype=torch.uint8, device="cuda")
+        big[chosen] = small.dev[name + "_pre"].view(4, -1)
+        scale = torch.full((experts, rows), float("nan"), device="cuda")
+        scale[chosen] = small.dev[name + "_scale"]
+        dev[name + "_pre"], dev[name + "_scale"] = big.view(-1), scale
+    assert dev["w1_pre"].numel() > 2 ** 32
+    wts = np.array([[0.5, 1.0, 0.25, 0.5]], np.float32)
+    args = (dev_u8(codes), fp8.E4M3, dev_f32(xs))
+    order = [2, 0, 3, 1]
+    out = hq.hq_moe_a8w8(*args, chosen[order].int()[None].contiguous(), dev_f32(wts), **dev)
+    ids = np.array([order], np.int32)
+    assert torch.equal(out, hq.hq_moe_a8w8(*args, torch.from_numpy(ids).cuda(), dev_f32(wts), **small.dev))
+    ref, _, _ = small.reference(v * xs[:, None], ids, wts)
+    _check_exact(out, ref)
 
 
 def test_layer_shares_the_gemm_workspace(hq):
