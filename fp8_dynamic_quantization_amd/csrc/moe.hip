@@ -280,18 +280,26 @@ struct MoeLds {
   uint32_t bits[kMoeMaxExperts / 32];
 };
 
-// Fills s; ends with a barrier.
-template <int THREADS>
+// Fills s, for the first kernel without the weights, for the second without the tokens'
+// scales; ends with a barrier. A thread's loads are under way before the first barrier.
+template <int THREADS, bool FIRST>
 __device__ __forceinline__ void moe_load_pairs(const MoeArgs& a, MoeLds& s) {
-  const int pairs = a.tokens * a.topk;
-  if (threadIdx.x < kMoeMaxExperts / 32) s.bits[threadIdx.x] = 0;
-  if ((int)threadIdx.x < a.tokens) s.x_scale[threadIdx.x] = a.x_scale[a.x_scale_per_row ? threadIdx.x : 0];
+  const int pairs = a.tokens * a.topk, t = threadIdx.x;
+  int e = t < pairs ? a.ids[t] : -1;
+  float w = !FIRST && t < pairs ? a.weights[t] : 0.0f;
+  const float xs = FIRST && t < a.tokens ? a.x_scale[a.x_scale_per_row ? t : 0] : 0.0f;
+  if (t < kMoeMaxExperts / 32) s.bits[t] = 0;
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += THREADS) {
-    const int e = a.ids[p];
+  if (FIRST && t < a.tokens) s.x_scale[t] = xs;
+  for (int p = t; p < pairs;) {
     s.ids[p] = e;
-    s.weights[p] = a.weights[p];
+    if (!FIRST) s.weights[p] = w;
     if ((unsigned)e < (unsigned)a.experts) atomicOr(&s.bits[e >> 5], 1u << (e & 31));
+    p += THREADS;
+    if (p < pairs) {
+      e = a.ids[p];
+      if (!FIRST) w = a.weights[p];
+    }
   }
   __syncthreads();
 }
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
   __shared__ __attribute__((aligned(16))) v4f red[kBufs][W > 1 ? W : 1][W > 1 ? 2 * MB : 1][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  moe_load_pairs<64 * W>(a, s);
+  moe_load_pairs<64 * W, true>(a, s);
   const ActiveExperts active(s);
   const int all = active.count * strips;
   if ((int)blockIdx.x * chunk >= all) return;
@@ -646,9 +654,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strip = blockIdx.x / splits, split = blockIdx.x % splits;
-  for (int i = lane; i < a.tokens * (kPitch / 4); i += 64)
-    *reinterpret_cast<v4f*>(&sums[wave][0][0] + 4 * i) = v4f{0.f, 0.f, 0.f, 0.f};
-  moe_load_pairs<64 * W>(a, s);
+  moe_load_pairs<64 * W, false>(a, s);
   const ActiveExperts active(s);
 
   const int K = a.inner, nkb = (K + kBK - 1) / kBK;
@@ -666,7 +672,13 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
   const int runs = splits * W, run = split * W + wave;
   const int first = (int)(items * run / runs), last = (int)(items * (run + 1) / runs);
 
-  if (first < last) {
+  auto clear_sums = [&]() {  // the wavefront's own
+    for (int i = lane; i < a.tokens * (kPitch / 4); i += 64)
+      *reinterpret_cast<v4f*>(&sums[wave][0][0] + 4 * i) = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  if (first >= last) {
+    clear_sums();
+  } else {
     struct Segment {  // a run's items of one expert: K blocks kb0 .. kb1 - 1
       int slot, e, rows, list, before, kb0, kb1;
     };
@@ -734,6 +746,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     enter(next, at);
     Chunk c0, c1;
     load(c0, next.kb0);
+    clear_sums();
     for (;;) {
       cur = next;
 #pragma unroll
@@ -836,7 +849,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 constexpr int kMoeCounters = 256;
 
 // The second kernel's workgroups: `strips` fragments times `splits`, of `waves`
-// wavefronts; 16 wavefronts per CU where the items suffice for two each.
+// wavefronts; 16 wavefronts per CU where the items suffice for four each. (Second kernel,
+// us, for two / four / sixteen each: 13 tokens, 24 of 1040 x 368 9.0 / 8.1 / 8.1; 2 tokens, 8 of
+// 2048 x 2048 7.6 / 6.7 / 6.7; 16 tokens, 128 of 512 x 512 10.0 / 10.0 / 13.2; 64 tokens, 8 of
+// 2048 x 2048 17.3 / 17.2 / 20.0.)
 struct MoePlan {
   int strips, splits, waves;
   size_t a_bytes, bytes;
@@ -849,7 +865,7 @@ static MoePlan moe_plan(int tokens, int topk, int experts, int hidden, int inner
   p.splits = 1;
   if (p.strips < kNumCUs) {
     const int64_t items = (int64_t)std::min(experts, pairs) * ((inner + kBK - 1) / kBK);
-    const int64_t worth = std::max<int64_t>(1, items / (2 * p.waves));
+    const int64_t worth = std::max<int64_t>(1, items / (4 * p.waves));
     p.splits = (int)std::min<int64_t>((kNumCUs + p.strips - 1) / p.strips, worth);
   }
   p.a_bytes = (size_t)pairs * moe_pitch(inner) * 2;
