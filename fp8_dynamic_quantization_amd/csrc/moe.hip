@@ -390,7 +390,9 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // end. The next block's weights and codes, also those of the next unit's first block,
 // are on their way while one is multiplied. Loads return in order, so the codes travel
 // with the weights: fetched when needed, they would wait for all weights in flight. Only
-// an expert's rows past 16, rare, are fetched that way. Codes are multiplied as f16, which
+// an expert's rows past 16, of more than 32 tokens, are fetched that way: a second block of
+// rows under way took 32 tokens, 32 experts of 7168 x 768 from 51 to 47 us, but spills with
+// four (64 tokens, 64 experts of 4096 x 1408 118 -> 122). Codes are multiplied as f16, which
 // holds each of them, so every product is exact and the sums are float32.
 // Bound by the weights of the experts that are asked for, each read once and past the
 // caches' own order (non-temporal: 117 us, else 130). 64 tokens, 64 experts of 4096 x 1408,
@@ -404,6 +406,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
   __shared__ MoeLds s;
   __shared__ int s_rows[2][W][kMoeMaxTokens];  // of two experts in turn
   __shared__ __attribute__((aligned(16))) v4f red[kBufs][W > 1 ? W : 1][W > 1 ? 2 * MB : 1][64];
+  constexpr int PB = MB == 2 ? 2 : 1;  // blocks of rows whose codes travel with the weights
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   moe_load_pairs<64 * W, true>(a, s);
@@ -426,7 +429,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
     const int r = 16 * i + xr;
     return r < u.rows ? s_rows[u.list][wave][r] / a.topk * K + xc : kBadOffset;
   };
-  int xo;  // the lane's first row
+  int xo[PB];  // the lane's rows of the first blocks
   auto enter = [&](Unit& u) {
     const int slot = u.at / strips;
     u.strip = u.at - slot * strips;
@@ -435,7 +438,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
       u.e = active.at(slot);
       u.list ^= 1;
       u.rows = moe_expert_rows(a, s, u.e, s_rows[u.list][wave], nullptr, u.before);
-      xo = row_offset(u, 0);
+#pragma unroll
+      for (int i = 0; i < PB; ++i) xo[i] = row_offset(u, i);
     }
 #pragma unroll
     for (int f = 0; f < 2; ++f)
@@ -450,7 +454,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
     }
   };
   struct Chunk {
-    uint4 w[2][2], x[2];
+    uint4 w[2][2], x[PB][2];
   };
   auto load = [&](Chunk& c, int kb) {
     const int wo = kb < nkb ? lane * 16 : kBadOffset;  // the scalar offset is not range-checked
@@ -459,7 +463,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         c.w[f][h] = as_uint4(__builtin_amdgcn_raw_buffer_load_b128(w_rsrc[f], wo + h * 1024, min(kb, nkb - 1) * kFragBytes, kNtLoad));
-    load_x(c.x, xo, kb);
+#pragma unroll
+    for (int i = 0; i < PB; ++i) load_x(c.x[i], xo[i], kb);
     __builtin_amdgcn_sched_barrier(0);  // ahead of the products that follow
   };
 
@@ -469,11 +474,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       uint4 late[2];
-      if (i > 0) {
-        if (16 * i >= cur.rows) break;  // wavefront-uniform
-        load_x(late, row_offset(cur, i), kb);
-      }
-      const uint4(&x)[2] = i > 0 ? late : c.x;
+      if (i > 0 && 16 * i >= cur.rows) break;  // wavefront-uniform
+      if (i >= PB) load_x(late, row_offset(cur, i), kb);
+      const uint4(&x)[2] = i >= PB ? late : c.x[i < PB ? i : 0];
       // 8 values of K per lane at a time: few converted codes are alive
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
