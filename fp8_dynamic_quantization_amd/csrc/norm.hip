@@ -12,7 +12,12 @@
 //   backward  xh = d * rstd, dx = dres + rstd * (t - mean_c t - xh * mean_c(t * xh)), db = sum_rows dy
 // Its sum of squares is taken of the differences, which the registers hold by then
 // (one more exchange across a row's wavefronts): sums of h and h^2 in one go cancel
-// where a row's mean is large beside its deviation.
+// where a row's mean is large beside its deviation. For the same reason the mean is
+// corrected by the mean of these differences, summed in the same exchange: the sum of
+// h is off by roundings of the mean's size, which may pass the deviation's (a constant
+// float32 row of 333333.34 came out as +-1). Without / with the correction, bf16 with
+// residual, h and copy, us in graphs: 1 x 7168 4.9 / 5.0, 1000 x 7168 11.2 / 11.9,
+// 16384 x 4096 84.2 / 85.2, 4096 x 16384 105.8 / 109.5, 2048 x 32768 136 / 118.
 //
 // All sums are float32; h enters the statistics and y unrounded.
 #include "hq_launch.h"
@@ -34,12 +39,24 @@ struct NormFwd {
   static constexpr int kThreads = kRowThreads * kRows;
 };
 
+// A layer norm's differences d = h - mean from their sum and that of their squares: the
+// mean's correction c = mean_c d, 0 where it is no number (rows whose codes are NaN
+// anyway), and sum (d - c)^2 = sum d^2 - c sum d. c is some units in the mean's last place,
+// so that this cancels in rows alone that are constant but for as much, and gives 0 exactly
+// in a constant one.
+__device__ __forceinline__ float mean_correction(float sum_d, int cols, float& sum_dd) {
+  float c = sum_d / (float)cols;
+  c = fabsf(c) < __builtin_inff() ? c : 0.0f;
+  if (sum_dd < __builtin_inff()) sum_dd = fmaxf(fmaf(-sum_d, c, sum_dd), 0.0f);
+  return c;
+}
+
 template <bool LN, int XT, int WPR, int NV>
 __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_kernel(NormArgs a) {
   using C = NormFwd<XT, WPR, NV>;
   constexpr int E = C::E;
   static_assert(WPR == 1 || C::kRows == 1, "one row per workgroup where a row needs its barrier");
-  __shared__ float s_sum[WPR], s_mean[LN ? WPR : 1];
+  __shared__ float s_sum[WPR], s_mean[LN ? WPR : 1], s_diff[LN ? WPR : 1];
   __shared__ uint32_t s_max[WPR], s_fin[WPR];
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % WPR);
   const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / C::kRowThreads);
@@ -119,7 +136,7 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_k
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), cs_rsrc, i / g * 4, 0, 0);
       }
     }
-    float mean = 0.0f;
+    float mean = 0.0f, total;
     if constexpr (LN) {
       if constexpr (kLate) {
         __builtin_amdgcn_sched_barrier(0);
@@ -127,20 +144,35 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_k
         __builtin_amdgcn_sched_barrier(0);
       }
       mean = row_sum_f32<WPR>(ss[0], s_mean, wave) / (float)a.cols;
+      // past the row's end v is 0 and stays it
+      auto inside = [&](int j) { return (t + j * C::kRowThreads) * E < a.cols; };
+      float sd[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const bool in = (t + j * C::kRowThreads) * E < a.cols;  // past the row's end the difference stays 0
-        ss[j] = 0.0f;
+        ss[j] = sd[j] = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          v[j][e] = in ? v[j][e] - mean : 0.0f;
+          v[j][e] -= inside(j) ? mean : 0.0f;
+          sd[j] += v[j][e];
           ss[j] = fmaf(v[j][e], v[j][e], ss[j]);
         }
       }
 #pragma unroll
-      for (int j = 1; j < NV; ++j) ss[0] += ss[j];
+      for (int j = 1; j < NV; ++j) {
+        ss[0] += ss[j];
+        sd[0] += sd[j];
+      }
+      float sum_d;
+      row_sum2_f32<WPR>(ss[0], sd[0], s_sum, s_diff, wave, &total, &sum_d);
+      const float c = mean_correction(sum_d, a.cols, total);
+      mean += c;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[j][e] -= inside(j) ? c : 0.0f;
+    } else {
+      total = row_sum_f32<WPR>(ss[0], s_sum, wave);
     }
-    const float total = row_sum_f32<WPR>(ss[0], s_sum, wave);
     const float rstd = 1.0f / sqrtf(fmaf(total, inv_n, a.eps));
     uint32_t m = 0;
 #pragma unroll
@@ -181,13 +213,13 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_k
 
 // Rows longer than the register form holds: one workgroup of 16 wavefronts per
 // row reads the row three times (sum of squares and checkpoint, maximum, cast
-// and h), for a layer norm four times (sum and checkpoint, sum of squares of the
-// differences, ...). h is written in the last pass only, each vector after its own reads,
+// and h), for a layer norm four times (sum and checkpoint, sums of the differences
+// and of their squares, ...). h is written in the last pass only, each vector after its own reads,
 // so h may be the residual's or x's own buffer here too.
 template <bool LN, int XT>
 __global__ __launch_bounds__(1024) void norm_quant_long_kernel(NormArgs a) {
   constexpr int E = VecTraits<XT>::kElems;
-  __shared__ float s_sum[16], s_mean[16];
+  __shared__ float s_sum[16], s_mean[16], s_diff[16];
   __shared__ uint32_t s_max[16], s_fin[16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = threadIdx.x;
@@ -228,19 +260,27 @@ __global__ __launch_bounds__(1024) void norm_quant_long_kernel(NormArgs a) {
         }
       }
     }
-    float mean = 0.0f;
+    float mean = 0.0f, c = 0.0f, total;  // a layer norm's first mean and its correction
     if constexpr (LN) {
       mean = row_sum_f32<16>(ss, s_mean, wave) / (float)a.cols;
+      float sd = 0.0f, sum_d;
       ss = 0.0f;
       for (int i = t; i < nvec; i += 1024) {
-        float v[E], p = 0.0f;
+        float v[E], p = 0.0f, q = 0.0f;
         load_h(i, v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) p = fmaf(v[e] - mean, v[e] - mean, p);
+        for (int e = 0; e < E; ++e) {
+          p = fmaf(v[e] - mean, v[e] - mean, p);
+          q += v[e] - mean;
+        }
         ss += p;
+        sd += q;
       }
+      row_sum2_f32<16>(ss, sd, s_sum, s_diff, wave, &total, &sum_d);
+      c = mean_correction(sum_d, a.cols, total);
+    } else {
+      total = row_sum_f32<16>(ss, s_sum, wave);
     }
-    const float total = row_sum_f32<16>(ss, s_sum, wave);
     const float rstd = 1.0f / sqrtf(fmaf(total, inv_n, a.eps));
     auto load_y = [&](int i, float* h, float* y) {
       load_h(i, h);
@@ -248,7 +288,7 @@ __global__ __launch_bounds__(1024) void norm_quant_long_kernel(NormArgs a) {
       const uint4 b = LN && bv ? bv[i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float d = LN ? h[e] - mean : h[e];
+        const float d = LN ? h[e] - mean - c : h[e];
         y[e] = wv ? d * rstd * vec_elem<XT>(w, e) : d * rstd;
         if constexpr (LN) y[e] += vec_elem<XT>(b, e);
       }
@@ -276,7 +316,7 @@ __global__ __launch_bounds__(1024) void norm_quant_long_kernel(NormArgs a) {
     if (t == 0) {
       a.scale[row] = s;
       if (a.rstd) a.rstd[row] = rstd;
-      if (LN && a.mean) a.mean[row] = mean;
+      if (LN && a.mean) a.mean[row] = mean + c;
     }
   }
 }

@@ -575,7 +575,9 @@ hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint
  *   mean = mean_c(h), rstd = 1 / sqrt(mean_c((h - mean)^2) + eps)
  *   y    = fl32(fl32((h - mean) * rstd) * weight) + bias
  *   q, scale_out = the per-token quantization of y, as hq_quantize_fp8
- * h is used unrounded, and the squares are summed of the differences. A NaN or an Inf
+ * h is used unrounded, the squares are summed of the differences, and the mean and
+ * the differences are corrected by the differences' own mean: a row whose mean is far
+ * larger than its deviation keeps its digits, and a constant one gives the bias. A NaN or an Inf
  * in a row, and a row whose sum passes float32's range, make the row's codes 0x7F and
  * its scale 2^-126; squares whose sum passes the range make rstd 0 and y the bias.
  *   bias       device, [cols] of xt, or NULL for zeros
