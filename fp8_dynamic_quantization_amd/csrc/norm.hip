@@ -458,9 +458,11 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a, int row_b
       if constexpr (CKPT) decode_vec<E>(hc[j], hs[j], xh[j]);
       else vec_widen<XT>(hv[j], xh[j]);
       float p = 0.0f, q = 0.0f;
+      // past the row's end, where h reads 0, nothing may pass float32's range: dy's 0 times it
+      const float m = (t + j * kRowThreads) * E < a.cols ? mean : 0.0f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        xh[j][e] = LN ? (xh[j][e] - mean) * rstd : xh[j][e] * rstd;
+        xh[j][e] = LN ? (xh[j][e] - m) * rstd : xh[j][e] * rstd;
         const float d = vec_elem<XT>(dy[j], e);
         const float tt = a.weight ? d * vec_elem<XT>(w[j], e) : d;
         p = fmaf(tt, xh[j][e], p);

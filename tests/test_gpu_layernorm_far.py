@@ -17,6 +17,7 @@ them are exact, and the corrected differences are zeros: y is the bias, bit for 
 """
 import numpy as np
 import pytest
+import torch
 
 import workloads
 from oracle import fp8, linear_ops as L, quantize as Q
@@ -75,3 +76,22 @@ def test_constant_bf16_sums(hq, cols):
     h = workloads.bf16_bits_to_f32(x) + workloads.bf16_bits_to_f32(r)
     out = hq.hq_layernorm_quantize_fp8(dev_bf16(x), None, None, EPS, residual=dev_bf16(r))
     assert np.array_equal(host(out.mean), h[:, 0]) and not fp8.decode(host(out.q), fp8.E4M3).any()
+
+
+@pytest.mark.parametrize("cols", [16, 48, 1040, 4112, 8208, 32784])
+@pytest.mark.parametrize("xt", [Q.F32, Q.BF16])
+def test_backward_of_far_constant_rows(hq, cols, xt):
+    """dx = rstd (t - mean(t)) whatever the constant: lanes past a row's end, which have no
+    h, add nothing, though (0 - mean) rstd passes float32's range there."""
+    rng = np.random.default_rng(cols)
+    c = 2.0 ** 120
+    h = torch.full((3, cols), c, dtype=torch.float32 if xt == Q.F32 else torch.bfloat16, device="cuda")
+    dy, dyv = _make(rng, (3, cols), xt)
+    mean, rstd = np.full(3, c, np.float32), np.full(3, 1e4, np.float32)
+    dx, dw, db = hq.hq_layernorm_backward(dy, h, None, dev_f32(mean), dev_f32(rstd))
+    d64 = dyv.astype(np.float64)
+    ref = 1e4 * (d64 - d64.mean(axis=1, keepdims=True))
+    terms = 1e4 * (np.abs(d64) + np.abs(d64).mean(axis=1, keepdims=True))
+    tol = D * terms + (0 if xt == Q.F32 else 2.0 ** -8) * (np.abs(ref) + D * terms) + U * np.abs(ref)
+    assert np.all(np.abs(_f64(dx) - ref) <= tol)
+    assert not host(dw).any() and np.all(np.abs(_f64(db) - d64.sum(axis=0)) <= 515 * U * np.abs(d64).sum(axis=0))
