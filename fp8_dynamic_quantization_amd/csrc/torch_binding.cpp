@@ -43,6 +43,13 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+// One of the ABI's enumerations: a number that would not survive the cast to int is
+// refused here, the others' range by the library.
+int choice(PyObject* o, const char* name) {
+  const int64_t v = integer(o);
+  TORCH_CHECK_VALUE(v == (int64_t)(int)v, name, " must fit in 32 bits, got ", v);
+  return (int)v;
+}
 double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -181,7 +188,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   want(n, 13);
   const Tensor x0 = tensor(a[0], "x"), w0 = maybe(a[1], "weight"), res0 = maybe(a[4], "residual");
   const float eps = (float)real(a[2]);
-  const int fmt = (int)integer(a[3]);
+  const int fmt = choice(a[3], "fmt");
   const bool write_h = a[6] == Py_True;
   const int64_t block = integer(a[9]);
   const Tensor cq = maybe(a[7], "checkpoint.q"), cs = maybe(a[8], "checkpoint.scales");
@@ -255,7 +262,7 @@ PyObject* layernorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   want(n, 15);
   const Tensor x0 = tensor(a[0], "x"), w0 = maybe(a[1], "weight"), b0 = maybe(a[2], "bias"), res0 = maybe(a[5], "residual");
   const float eps = (float)real(a[3]);
-  const int fmt = (int)integer(a[4]);
+  const int fmt = choice(a[4], "fmt");
   const bool write_h = a[7] == Py_True;
   const int64_t block = integer(a[10]);
   const Tensor cq = maybe(a[8], "checkpoint.q"), cs = maybe(a[9], "checkpoint.scales");
@@ -333,8 +340,9 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   want(nargs, 16);
   const Tensor xq0 = tensor(a[0], "xq"), wp = tensor(a[2], "wq_pre"), xs0 = tensor(a[4], "x_scale"), ws0 = tensor(a[5], "w_scale");
-  const int xf = (int)integer(a[1]), wf = (int)integer(a[3]), act = (int)integer(a[10]), out_fmt = (int)integer(a[13]);
-  const int64_t n = integer(a[6]), bias_type = integer(a[8]);
+  const int xf = choice(a[1], "xf"), wf = choice(a[3], "wf"), act = choice(a[10], "act"), out_fmt = choice(a[13], "out_fmt");
+  const int64_t n = integer(a[6]);
+  const int bias_type = choice(a[8], "bias_type");
   const Tensor bias0 = maybe(a[7], "bias"), bs0 = maybe(a[9], "bias_scale"), res0 = maybe(a[11], "residual");
   const Tensor os0 = maybe(a[12], "out_scale");
   const bool shared = a[15] == Py_None;
@@ -377,7 +385,7 @@ PyObject* gemm_fused(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   hq_status st;
   {
     const NoGil nogil;
-    const hq_fused_epilogue ep = {ptr(bias), (int32_t)bias_type, ptr<float>(bs), ptr<float>(os), out_fmt, act, ptr<uint16_t>(res)};
+    const hq_fused_epilogue ep = {ptr(bias), bias_type, ptr<float>(bs), ptr<float>(os), out_fmt, act, ptr<uint16_t>(res)};
     st = hq_gemm_a8w8_fused(ptr<uint8_t>(xq), xf, ptr<uint8_t>(wp), wf, ptr<float>(xs), xs.numel(), ptr<float>(ws), ws.numel(), m,
                             n, k, &ep, ptr(out), ptr(work), bytes_of(work), stream_of(xq));
   }
@@ -391,7 +399,7 @@ PyObject* act_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 9);
   const Tensor z0 = tensor(a[0], "z");
-  const int act = (int)integer(a[1]), fmt = (int)integer(a[2]);
+  const int act = choice(a[1], "act"), fmt = choice(a[2], "fmt");
   const bool gated = a[3] == Py_True;
   const int64_t block = integer(a[6]);
   const Tensor cq = maybe(a[4], "checkpoint.q"), cs = maybe(a[5], "checkpoint.scales");
@@ -425,7 +433,7 @@ PyObject* act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t block = integer(a[3]);
   TORCH_CHECK_VALUE(block != 0, "z must be a checkpoint");
   const Tensor cq = maybe(a[1], "checkpoint.q"), cs = maybe(a[2], "checkpoint.scales");
-  const int act = (int)integer(a[4]);
+  const int act = choice(a[4], "act");
   const bool gated = a[5] == Py_True, sum = a[8] == Py_True;
   Tensor dz = maybe(a[6], "dz"), db = maybe(a[7], "dbias");
   hq_status st;
@@ -454,7 +462,7 @@ PyObject* wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   want(nargs, 9);
   const Tensor g0 = tensor(a[0], "g"), xq0 = tensor(a[1], "xq"), xs0 = tensor(a[3], "x_scale"), base0 = maybe(a[5], "base");
-  const int xf = (int)integer(a[2]), dwt = (int)integer(a[4]);
+  const int xf = choice(a[2], "xf"), dwt = choice(a[4], "dwt");
   const bool allocate = a[7] == Py_None, strict = a[8] == Py_True;
   const Tensor given = a[7] == Py_False ? Tensor() : maybe(a[7], "workspace");
   Tensor dw = maybe(a[6], "dw");
@@ -495,7 +503,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   want(n, 6);
   const Tensor l0 = tensor(a[0], "logits");
   const int64_t topk = integer(a[1]);
-  const int score = (int)integer(a[2]);
+  const int score = choice(a[2], "score");
   const bool renorm = a[3] == Py_True;
   Tensor ids = maybe(a[4], "ids"), w = maybe(a[5], "weights");
   hq_status st;
@@ -521,7 +529,7 @@ PyObject* moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   want(n, 6);
   const Tensor l0 = tensor(a[0], "logits"), ids0 = tensor(a[1], "ids"), dw0 = tensor(a[2], "dweights");
-  const int score = (int)integer(a[3]);
+  const int score = choice(a[3], "score");
   const bool renorm = a[4] == Py_True;
   Tensor dl = maybe(a[5], "dlogits");
   hq_status st;
@@ -565,7 +573,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   want(nargs, 18);
   const Tensor xq0 = tensor(a[0], "xq"), xs0 = tensor(a[2], "x_scale"), ids0 = tensor(a[3], "ids"), wt0 = tensor(a[4], "weights");
   const Tensor w1 = tensor(a[5], "w1_pre"), s10 = tensor(a[6], "w1_scale"), w2 = tensor(a[7], "w2_pre"), s20 = tensor(a[8], "w2_scale");
-  const int xf = (int)integer(a[1]), wf = (int)integer(a[9]), act = (int)integer(a[11]);
+  const int xf = choice(a[1], "xf"), wf = choice(a[9], "wf"), act = choice(a[11], "act");
   const int64_t inner = integer(a[10]);
   const bool gated = a[12] == Py_True;
   const Tensor b10 = maybe(a[13], "bias1"), b20 = maybe(a[14], "bias2"), res0 = maybe(a[15], "residual");
