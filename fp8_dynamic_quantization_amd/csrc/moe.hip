@@ -852,7 +852,12 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 constexpr int kMoeCounters = 256;
 
 // The second kernel's workgroups: `strips` fragments times `splits`, of `waves`
-// wavefronts; 16 wavefronts per CU where the items suffice for four each. (Second kernel,
+// wavefronts; 16 wavefronts per CU where the items suffice for four each. One workgroup of
+// 16 wavefronts fits on a CU, so there are never more of them than CUs: the few past the
+// device would take as long again (32 experts of hidden x 1536, top 4, call in a graph, us,
+// at most / at least 256 workgroups: 16 tokens 768 24.8 / 28.9, 1040 28.0 / 35.5, 2080
+// 39.5 / 47.7, 3584 63.7 / 69.3; 64 tokens 44.9 / 51.3, 48.3 / 60.3, 79.1 / 100.6, 85.4 / 103.7;
+// 1024, 2048 and 4096 are the same in both). (Second kernel,
 // us, for two / four / sixteen each: 13 tokens, 24 of 1040 x 368 9.0 / 8.1 / 8.1; 2 tokens, 8 of
 // 2048 x 2048 7.6 / 6.7 / 6.7; 16 tokens, 128 of 512 x 512 10.0 / 10.0 / 13.2; 64 tokens, 8 of
 // 2048 x 2048 17.3 / 17.2 / 20.0.)
@@ -869,7 +874,7 @@ static MoePlan moe_plan(int tokens, int topk, int experts, int hidden, int inner
   if (p.strips < kNumCUs) {
     const int64_t items = (int64_t)std::min(experts, pairs) * ((inner + kBK - 1) / kBK);
     const int64_t worth = std::max<int64_t>(1, items / (4 * p.waves));
-    p.splits = (int)std::min<int64_t>((kNumCUs + p.strips - 1) / p.strips, worth);
+    p.splits = (int)std::min<int64_t>(kNumCUs / p.strips, worth);
   }
   p.a_bytes = (size_t)pairs * moe_pitch(inner) * 2;
   p.bytes = kMoeCounters * 4 + p.a_bytes + (p.splits > 1 ? (size_t)p.strips * p.splits * tokens * 16 * sizeof(float) : 0);

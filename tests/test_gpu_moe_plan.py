@@ -1,0 +1,37 @@
+"""The expert layer where its second kernel is divided over workgroups at widths that do not
+divide the device, on an MI355X; results
+bit for bit (see test_gpu_moe)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8
+from tests.gpu_helpers import dev_f32, dev_u8, require_gpu
+from tests.test_gpu_moe import _check_exact, _choose, _exact_layer, _exact_tokens
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hq():
+    return require_gpu()
+
+
+def _run(hq, layer, codes, xs, ids, wts):
+    return hq.hq_moe_a8w8(dev_u8(codes), fp8.E4M3, dev_f32(xs), torch.from_numpy(ids).cuda(), dev_f32(wts), **layer.dev)
+
+
+# two to five workgroups a fragment, and one of them past 128 fragments; each count of row blocks
+@pytest.mark.parametrize("tokens,hidden", [(16, 768), (64, 768), (16, 1040), (40, 1040), (24, 1536), (64, 288), (20, 2048), (9, 1360),
+                                           (33, 2064)])
+def test_divided_widths(hq, tokens, hidden):
+    rng = np.random.default_rng(hidden + tokens)
+    layer = _exact_layer(hq, rng, 40, hidden, 1024, False)
+    codes, xs, v = _exact_tokens(rng, tokens, hidden)
+    ids, wts = _choose(rng, tokens, 40, 5)
+    strips = 2 * -(-hidden // 32)
+    extra = hq.hq_moe_workspace_bytes(tokens, 5, 40, hidden, 1024) - 1024 - tokens * 5 * 1024 * 2
+    assert (extra > 0) == (strips <= 128)
+    out = _run(hq, layer, codes, xs, ids, wts)
+    _check_exact(out, layer.reference(v * xs[:, None], ids, wts)[0])
+    assert torch.equal(out, _run(hq, layer, codes, xs, ids, wts))
