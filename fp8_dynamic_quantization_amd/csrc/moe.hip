@@ -385,7 +385,9 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // A unit is two weight fragments of one expert: 16 columns of the first half and the
 // same columns of the second (gated), or 32 columns. The units that the step asks for
 // are dealt over the workgroups, which fill the device once, in chunks of neighbours
-// (an expert with many rows takes longer: its units go to many workgroups). A
+// (an expert with many rows takes longer: its units go to many workgroups), four chunks
+// a workgroup of what is asked for: chunks of what 64 tokens could ask for left a padded
+// batch of one to 102 workgroups (8 of 256 experts 2048 x 2048, call 54 us, so 30). A
 // workgroup's W wavefronts take a unit's K blocks w, w + W, ... and meet in LDS at its
 // end. The next block's weights and codes, also those of the next unit's first block,
 // are on their way while one is multiplied. Loads return in order, so the codes travel
@@ -399,8 +401,7 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // 58 asked for, 669 MB: 117 us, 5.7 TB/s; 1 token, 8 of them, 92 MB: 18 us, 5.1 TB/s. Below
 // some 10 MB a launch, the pairs and one trip to memory: 5 to 6 us.
 template <int XF, int WF, int MB, bool GATED, int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ? 3 : 4))) void moe_up_kernel(MoeArgs a, int strips, int chunk,
-                                                                                                   int act) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ? 3 : 4))) void moe_up_kernel(MoeArgs a, int strips, int act) {
   // two buffers for the sums save a barrier; with more row blocks they would cost a workgroup per CU
   constexpr int kBufs = W > 1 && MB == 1 ? 2 : 1;
   __shared__ MoeLds s;
@@ -412,6 +413,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
   moe_load_pairs<64 * W, true>(a, s);
   const ActiveExperts active(s);
   const int all = active.count * strips;
+  const int chunk = max(1, all / (4 * (int)gridDim.x));
   if ((int)blockIdx.x * chunk >= all) return;
 
   const int K = a.hidden, nkb = (K + kBK - 1) / kBK;
@@ -888,9 +890,8 @@ template <int XF, int WF, int MB, int W>
 static hipError_t launch_moe_up_w(const MoeArgs& a, int act, bool gated, int strips, int units, hipStream_t st) {
   constexpr int kResident = (MB > 1 ? 12 : 16) * kNumCUs / W;  // workgroups that the registers hold at once
   const int groups = std::min(units, kResident);
-  const int chunk = std::max(1, units / (4 * groups));
-  if (gated) hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, true, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, chunk, act);
-  else hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, false, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, chunk, act);
+  if (gated) hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, true, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, act);
+  else hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, false, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, act);
   return hipGetLastError();
 }
 

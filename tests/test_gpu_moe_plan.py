@@ -1,6 +1,6 @@
 """The expert layer where its second kernel is divided over workgroups at widths that do not
-divide the device, on an MI355X; results
-bit for bit (see test_gpu_moe)."""
+divide the device, and where a batch asks for few of many experts, on an MI355X; results bit
+for bit (see test_gpu_moe)."""
 import numpy as np
 import pytest
 import torch
@@ -35,3 +35,24 @@ def test_divided_widths(hq, tokens, hidden):
     out = _run(hq, layer, codes, xs, ids, wts)
     _check_exact(out, layer.reference(v * xs[:, None], ids, wts)[0])
     assert torch.equal(out, _run(hq, layer, codes, xs, ids, wts))
+
+
+@pytest.mark.parametrize("kind", ["one of 64", "all alike", "one of the last", "first and last experts"])
+def test_few_of_many_experts(hq, kind):
+    """A layer whose first kernel deals its units in chunks, asked for little: a batch padded
+    with slots of no expert, and tokens that all choose the same."""
+    rng = np.random.default_rng(7)
+    layer = _exact_layer(hq, rng, 400, 16, 1024, True)
+    codes, xs, v = _exact_tokens(rng, 64, 16)
+    ids, wts = _choose(rng, 64, 400, 8)
+    if kind == "one of 64":
+        ids[1:] = -1
+    elif kind == "all alike":
+        ids[:] = ids[0]
+    elif kind == "one of the last":
+        ids[:] = -1
+        ids[63, 7] = 399
+    else:
+        ids[:] = [0, 399, -1, -1, 0, 399, 1 << 20, -1]
+    out = _run(hq, layer, codes, xs, ids, wts)
+    _check_exact(out, layer.reference(v * xs[:, None], ids, wts)[0])
