@@ -888,7 +888,11 @@ size_t moe_workspace_bytes(int tokens, int topk, int experts, int hidden, int in
 
 template <int XF, int WF, int MB, int W>
 static hipError_t launch_moe_up_w(const MoeArgs& a, int act, bool gated, int strips, int units, hipStream_t st) {
-  constexpr int kResident = (MB > 1 ? 12 : 16) * kNumCUs / W;  // workgroups that the registers hold at once
+  // As many as the registers hold at once: 16 or 12 wavefronts per CU. (Past 32 tokens workgroups
+  // of 8 wavefronts fit once on a CU, and up to 128 of them take the places of those that end. With
+  // 256, us for 64 tokens of 8 experts: 7168 x 768 41.4 -> 51.6, 4096 x 640 28.3 -> 30.5, 2048 x 992
+  // 24.4 -> 23.1.)
+  constexpr int kResident = (MB > 1 ? 12 : 16) * kNumCUs / W;
   const int groups = std::min(units, kResident);
   if (gated) hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, true, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, act);
   else hipLaunchKernelGGL((moe_up_kernel<XF, WF, MB, false, W>), dim3(groups), dim3(64 * W), 0, st, a, strips, act);
@@ -896,11 +900,15 @@ static hipError_t launch_moe_up_w(const MoeArgs& a, int act, bool gated, int str
 }
 
 // Wavefronts per unit: enough K blocks for two or more each, and enough wavefronts for the
-// device where units are few. Measured (us, 1 / 2 / 4 / 8; before the last steps above): 16 of
-// 128 experts 512 x 512 8.5 / 8.4 / 9.2 / 37; 40 tokens, 100 experts 256 x 2048 16.0 / 28.5 /
-// 39.9 / 140; 64 tokens, 8 experts 2048 x 2048 28.6 / 28.0 / 19.6 / 28.1; 1 token, 32 experts
-// 7168 x 768 (192 units) 29.2 / 18.3 / 13.1 / 10.4; 1 token, 64 experts 4096 x 1408 (704
-// units) 23.6 / 18.2 / 18.0 / 24.3.
+// device where units are few. Measured (call in a graph, us, with 1 / 2 / 4 / 8): 16 of 128
+// experts 512 x 512 18.1 / 18.3 / 20.5 / 26.9; 40 tokens, 100 experts 256 x 2048 34.9 / 38.3 /
+// 49.1 / 113; 64 tokens, 8 experts 2048 x 2048 46.3 / 41.3 / 36.5 / 44.5; 64 experts 4096 x 1408,
+// 1 token (704 units) 33.0 / 29.1 / 29.0 / 28.8 and 64 tokens 220 / 204 / 194 / 237; 1 token, 32
+// experts 7168 x 768 (192 units) 36.7 / 25.6 / 20.2 / 18.2. At 17 to 32 tokens a CU holds one
+// workgroup of 8 or three of 4, which are ahead where the units are more than the CUs (4 / 8,
+// 32 tokens of 8 experts: 320 units 4096 x 640 19.8 / 22.7; 384 units 2048 x 768 14.9 / 18.0, 7168 x
+// 768 31.9 / 34.0; 192 units 7168 x 384 20.9 / 19.7). Past 32 tokens neither is ahead between one
+// and two units per CU (2048 x 992 22.4 / 24.4, 3584 x 768 29.6 / 27.2, 7168 x 768 55.0 / 41.4).
 template <int XF, int WF, int MB>
 static hipError_t launch_moe_up(const MoeArgs& a, int act, bool gated, hipStream_t st) {
   const int strips = gated ? a.inner / 16 : (a.inner + 31) / 32;
@@ -908,7 +916,7 @@ static hipError_t launch_moe_up(const MoeArgs& a, int act, bool gated, hipStream
   const int nkb = (a.hidden + kBK - 1) / kBK;
   if (nkb <= 2) return launch_moe_up_w<XF, WF, MB, 1>(a, act, gated, strips, units, st);
   if (nkb <= 4) return launch_moe_up_w<XF, WF, MB, 2>(a, act, gated, strips, units, st);
-  if (units >= 2 * kNumCUs || nkb <= 8) return launch_moe_up_w<XF, WF, MB, 4>(a, act, gated, strips, units, st);
+  if (units >= (MB == 2 ? kNumCUs + 1 : 2 * kNumCUs) || nkb <= 8) return launch_moe_up_w<XF, WF, MB, 4>(a, act, gated, strips, units, st);
   return launch_moe_up_w<XF, WF, MB, 8>(a, act, gated, strips, units, st);
 }
 

@@ -56,3 +56,15 @@ def test_few_of_many_experts(hq, kind):
         ids[:] = [0, 399, -1, -1, 0, 399, 1 << 20, -1]
     out = _run(hq, layer, codes, xs, ids, wts)
     _check_exact(out, layer.reference(v * xs[:, None], ids, wts)[0])
+
+
+@pytest.mark.parametrize("tokens", [8, 24, 48])
+@pytest.mark.parametrize("inner", [480, 544, 1056])
+def test_wavefronts_per_unit(hq, tokens, inner):
+    """240, 272 and 528 units of 9 K blocks: either side of where each count of row blocks
+    takes fewer wavefronts for a unit."""
+    rng = np.random.default_rng(inner)
+    layer = _exact_layer(hq, rng, 8, 1040, inner, True)
+    codes, xs, v = _exact_tokens(rng, tokens, 1040)
+    ids, wts = _choose(rng, tokens, 8, 3)
+    _check_exact(_run(hq, layer, codes, xs, ids, wts), layer.reference(v * xs[:, None], ids, wts)[0])
