@@ -345,13 +345,13 @@ __device__ __forceinline__ int moe_place(int n, int r, int col) {
   return ((col >> 7) * 16 + (col >> 3 & 3) * 4 + (col >> 5 & 3)) * n * 8 + r * 8 + (col & 7);
 }
 
-// The tokens that chose expert e, in order: their first pair with it and, where wts is
-// not null, the sum of their weights for it (a token that names an expert twice has one
-// row). rows and wts have 64 entries of this wavefront's own; before: the pairs that chose
+// The tokens that chose expert e, in order, and, where wts is not null, the sum of their
+// weights for it (a token that names an expert twice has one row). rows and wts have 64 entries of this wavefront's own; before: the pairs that chose
 // an expert below e, where the expert's rows of activations start.
 __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s, int e, int* rows, float* wts, int& before) {
   const int t = threadIdx.x & 63;
-  int p = -1, below = 0;
+  bool mine = false;
+  int below = 0;
   float w = 0.0f;
   for (int j0 = 0; j0 < a.topk; j0 += 4) {
 #pragma unroll
@@ -360,16 +360,16 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
       const int id = t < a.tokens && j < a.topk ? s.ids[q] : -1;
       below += __popcll(__ballot((unsigned)id < (unsigned)e));
       if (id == e) {
-        if (p < 0) p = q;
+        mine = true;
         if (wts) w += s.weights[q];
       }
     }
   }
   before = below;
-  const uint64_t m = __ballot(p >= 0);
-  if (p >= 0) {
+  const uint64_t m = __ballot(mine);
+  if (mine) {
     const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-    rows[at] = p;
+    rows[at] = t;
     if (wts) wts[at] = w;
   }
   // LDS operations of one wavefront complete in order
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
   __amdgpu_buffer_rsrc_t w_rsrc[2];
   auto row_offset = [&](const Unit& u, int i) {
     const int r = 16 * i + xr;
-    return r < u.rows ? s_rows[u.list][wave][r] / a.topk * K + xc : kBadOffset;
+    return r < u.rows ? s_rows[u.list][wave][r] * K + xc : kBadOffset;
   };
   int xo[PB];  // the lane's rows of the first blocks
   auto enter = [&](Unit& u) {
@@ -522,8 +522,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ?
       const int i = GATED ? part : part >> 1;
       if ((W > 1 && (part + turn) % W != wave) || 16 * i >= cur.rows) continue;
       const int r = 16 * i + xr;
-      const int pair = s_rows[cur.list][wave][min(r, cur.rows - 1)];
-      const float xs = s.x_scale[pair / a.topk];
+      const float xs = s.x_scale[s_rows[cur.list][wave][min(r, cur.rows - 1)]];
       float z[2][4];
 #pragma unroll
       for (int f = 0; f < (GATED ? 2 : 1); ++f) {
@@ -782,7 +781,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
         const int r = 16 * i + xr;
         if (r >= cur.rows) continue;
         const float wt = s_wts[cur.list][wave][r];
-        v4f* p = reinterpret_cast<v4f*>(&sums[wave][s_rows[cur.list][wave][r] / a.topk][4 * xq]);
+        v4f* p = reinterpret_cast<v4f*>(&sums[wave][s_rows[cur.list][wave][r]][4 * xq]);
         v4f t = *p;
         const bool biased = a.b2 && cur.kb0 == 0;  // with the expert's first K block
 #pragma unroll
