@@ -22,7 +22,11 @@ namespace hq {
 // dependent lane moves take (1 token, 128 experts, topk 8: 3.6 us in a graph, bf16 3.0);
 // beyond, the rounds' vector instructions bound it, not the 9.4 MB: 16384 tokens, 128
 // experts, topk 8, float32 6.2 us, bf16, whose keys hold the index, 5.2 (7.0 both with
-// floats compared).
+// floats compared). 512 and 1024 experts and 16 slots alike: a wavefront has one token and
+// issues some 250 vector instructions for 8 logits a lane (450 for 16) before the rounds, 52 (88; bf16
+// 51) and four (bf16 two) exchanges through LDS in each, and 200 after them. 16 tokens a SIMD at 4 cycles each make
+// 16384 tokens 34 us with 512 experts, topk 16 (29.6 measured), and 36 (bf16 29) with 1024,
+// topk 8 (36.9 and 25.7). The backward pass issues some 800 with 1024 experts: 21 us (17.8).
 constexpr int kMaxTopk = 16;
 
 template <int G, class F>
@@ -398,7 +402,7 @@ __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s
 // holds each of them, so every product is exact and the sums are float32.
 // Bound by the weights of the experts that are asked for, each read once and past the
 // caches' own order (non-temporal: 117 us, else 130). 64 tokens, 64 experts of 4096 x 1408,
-// 58 asked for, 669 MB: 117 us, 5.7 TB/s; 1 token, 8 of them, 92 MB: 18 us, 5.1 TB/s. Below
+// 58 asked for, 669 MB: 115 us, 5.8 TB/s; 1 token, 8 of them, 92 MB: 17.7 us, 5.2 TB/s. Below
 // some 10 MB a launch, the pairs and one trip to memory: 5 to 6 us.
 template <int XF, int WF, int MB, bool GATED, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(MB > 1 ? 3 : 4))) void moe_up_kernel(MoeArgs a, int strips, int act) {
@@ -632,7 +636,9 @@ __device__ __forceinline__ b8v bf16x8(uint32_t d0, uint32_t d1) {
 // A workgroup owns one weight fragment (16 output columns) of every expert, and all
 // tokens; the (expert, K block) items are dealt in runs over its W wavefronts and over
 // `splits` workgroups. The next item's operands are on their way while one is
-// multiplied (rows past 16 as above). A wavefront adds an expert's weighted rows into
+// multiplied; an expert's rows past 16 are all fetched when they are (at 17 to 32 tokens
+// 120 of 128 registers are taken, a second block under way has 16; past 32 tokens 12 bytes a
+// lane are in scratch memory as it is). A wavefront adds an expert's weighted rows into
 // sums of its own in LDS ([token][column], 16 MB tokens), so no two lanes meet; at the end
 // the wavefronts' sums are added in order, and with splits > 1 the last workgroup to
 // arrive adds the workgroups' sums, in order too: the result does not depend on who ends

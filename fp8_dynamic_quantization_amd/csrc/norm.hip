@@ -14,10 +14,10 @@
 // (one more exchange across a row's wavefronts): sums of h and h^2 in one go cancel
 // where a row's mean is large beside its deviation. For the same reason the mean is
 // corrected by the mean of these differences, summed in the same exchange: the sum of
-// h is off by roundings of the mean's size, which may pass the deviation's (a constant
-// float32 row of 333333.34 came out as +-1). Without / with the correction, bf16 with
-// residual, h and copy, us in graphs: 1 x 7168 4.9 / 5.0, 1000 x 7168 11.2 / 11.9,
-// 16384 x 4096 84.2 / 85.2, 4096 x 16384 105.8 / 109.5, 2048 x 32768 136 / 118.
+// h is off by roundings of the mean's size, which may pass the deviation's (of constant
+// float32 rows of 1040, 12345.678 came out as -0.3 and -7.7e7 as -1). Without / with the
+// correction, bf16 with residual, h and copy, us in graphs: 1 x 7168 4.9 / 5.0, 1000 x 7168
+// 11.2 / 11.9, 16384 x 4096 84.2 / 85.2, 4096 x 16384 105.8 / 109.5, 2048 x 32768 136 / 118.
 //
 // All sums are float32; h enters the statistics and y unrounded.
 #include "hq_launch.h"
@@ -79,9 +79,11 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_k
     }
   };
   // A layer norm of 16-bit rows with several vectors per thread fetches weight and bias
-  // with each row, after its sum: held over the row's loads they cost a wavefront per
-  // SIMD or two (us, held / fetched: 16384 x 4096 86.2 / 83.8, 8192 x 7168 84.0 / 74.1,
-  // 16384 x 2048 45.9 / 43.6; 16384 x 1024 22.7 / 23.5 and float32 8192 x 4096 70.8 / 72.9).
+  // with each row, after its sum: held over the row's loads they cost a wavefront per SIMD or
+  // two, or spills. With residual, h and copy, us in graphs over one set of tensors (whose part
+  // in the Infinity Cache makes the large ones faster than HBM alone), held / fetched: 16384 x 4096
+  // 88.3 / 85.8, 8192 x 7168 86.1 / 76.0, 16384 x 2048 47.5 / 44.4, 2048 x 32768 292 / 118;
+  // 16384 x 1024 23.1 / 23.8 and float32 8192 x 4096 71.3 / 73.9, which hold them.
   constexpr bool kLate = LN && XT == kBF16 && NV >= 2 && WPR * NV > 2;
   if constexpr (!kLate) load_affine();
 
@@ -704,7 +706,9 @@ static hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
 // two wavefronts per SIMD. Where two forms serve one width the first is for few
 // rows, whose latency counts (us, 7168 columns: one row 3.9 with 8 x 2 and 4.7
 // with 4 x 4, 4681 rows 53.2 and 51.1; 2048 columns: 1000 rows 4.8 with 4 x 1 and
-// 5.4 with 1 x 4, 16384 rows 53.0 and 49.3).
+// 5.4 with 1 x 4, 16384 rows 53.0 and 49.3). The form of 16 x 4 spills with bf16 rows,
+// 100 bytes a lane for an RMS norm and 16 for a layer norm; the backward pass's of 16 x 2
+// for a layer norm alone, 24 bytes and 60 from the copy.
 template <bool LN, int XT>
 static hipError_t launch_norm_x(const NormArgs& a, hipStream_t st) {
   const int nvec = a.cols / VecTraits<XT>::kElems;

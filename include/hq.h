@@ -577,7 +577,8 @@ hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint
  *   q, scale_out = the per-token quantization of y, as hq_quantize_fp8
  * h is used unrounded, the squares are summed of the differences, and the mean and
  * the differences are corrected by the differences' own mean: a row whose mean is far
- * larger than its deviation keeps its digits, and a constant one gives the bias. A NaN or an Inf
+ * larger than its deviation keeps its digits, and a constant one gives the bias (NaN
+ * with eps 0). A NaN or an Inf
  * in a row, and a row whose sum passes float32's range, make the row's codes 0x7F and
  * its scale 2^-126; squares whose sum passes the range make rstd 0 and y the bias.
  *   bias       device, [cols] of xt, or NULL for zeros
@@ -735,7 +736,8 @@ typedef enum hq_route { HQ_ROUTE_SOFTMAX = 0, HQ_ROUTE_SIGMOID = 1 } hq_route;
  *   p       = exp(l - max) / sum over all experts, or 1 / (1 + exp(-l))
  *   weights = p, or with `renormalize` p / (sum of the chosen experts' p)
  * An expert whose logit is -Inf or NaN is never chosen and has p = 0; slots left over
- * get id -1 and weight 0. Logits of +Inf share the weight among themselves.
+ * get id -1 and weight 0. Logits of +Inf: the softmax shares its weight among them
+ * alone, the logistic score of each is 1.
  *   logits   device, [tokens, num_experts] of xt, row-major
  *   score    an hq_route value; renormalize 0 or 1
  *   ids      device, int32 [tokens, topk]
