@@ -578,9 +578,9 @@ hq_status hq_rmsnorm_backward(const void* dy, const void* h, const hq_checkpoint
  * h is used unrounded, the squares are summed of the differences, and the mean and
  * the differences are corrected by the differences' own mean: a row whose mean is far
  * larger than its deviation keeps its digits, and a constant one gives the bias (NaN
- * with eps 0). A NaN or an Inf
- * in a row, and a row whose sum passes float32's range, make the row's codes 0x7F and
- * its scale 2^-126; squares whose sum passes the range make rstd 0 and y the bias.
+ * with eps 0). A NaN or an Inf in a row, and a row whose sum passes float32's range,
+ * make the row's codes 0x7F and its scale 2^-126; squares whose sum passes the range
+ * make rstd 0 and y the bias.
  *   bias       device, [cols] of xt, or NULL for zeros
  *   mean_out   device, float32 [rows], or NULL (the backward pass needs it)
  * All other arguments, and the requirements, are those of hq_rmsnorm_quantize_fp8.
