@@ -22,11 +22,12 @@ namespace hq {
 // dependent lane moves take (1 token, 128 experts, topk 8: 3.6 us in a graph, bf16 3.0);
 // beyond, the rounds' vector instructions bound it, not the 9.4 MB: 16384 tokens, 128
 // experts, topk 8, float32 6.2 us, bf16, whose keys hold the index, 5.2 (7.0 both with
-// floats compared). 512 and 1024 experts and 16 slots alike: a wavefront has one token and
-// issues some 250 vector instructions for 8 logits a lane (450 for 16) before the rounds, 52 (88; bf16
-// 51) and four (bf16 two) exchanges through LDS in each, and 200 after them. 16 tokens a SIMD at 4 cycles each make
-// 16384 tokens 34 us with 512 experts, topk 16 (29.6 measured), and 36 (bf16 29) with 1024,
-// topk 8 (36.9 and 25.7). The backward pass issues some 800 with 1024 experts: 21 us (17.8).
+// floats compared). So are 512 and 1024 experts, and 16 slots: a wavefront has one token and
+// issues some 270 vector instructions for 8 logits a lane (480 for 16) before the rounds, 52
+// (88; bf16 51) and four (bf16 two) exchanges through LDS in each, and 200 after them. 16
+// tokens a SIMD at 4 cycles an instruction make 16384 tokens 34 us with 512 experts, topk 16
+// (29.6 measured), and 36 (bf16 29) with 1024, topk 8 (36.9 and 25.7). The backward pass
+// issues some 800 with 1024 experts: 21 us (17.8).
 constexpr int kMaxTopk = 16;
 
 template <int G, class F>
@@ -350,8 +351,9 @@ __device__ __forceinline__ int moe_place(int n, int r, int col) {
 }
 
 // The tokens that chose expert e, in order, and, where wts is not null, the sum of their
-// weights for it (a token that names an expert twice has one row). rows and wts have 64 entries of this wavefront's own; before: the pairs that chose
-// an expert below e, where the expert's rows of activations start.
+// weights for it (a token that names an expert twice has one row). rows and wts have 64
+// entries of this wavefront's own; before: the pairs that chose an expert below e, where the
+// expert's rows of activations start.
 __device__ __forceinline__ int moe_expert_rows(const MoeArgs& a, const MoeLds& s, int e, int* rows, float* wts, int& before) {
   const int t = threadIdx.x & 63;
   bool mine = false;

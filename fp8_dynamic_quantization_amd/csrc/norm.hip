@@ -146,7 +146,7 @@ __global__ __launch_bounds__((NormFwd<XT, WPR, NV>::kThreads)) void norm_quant_k
         __builtin_amdgcn_sched_barrier(0);
       }
       mean = row_sum_f32<WPR>(ss[0], s_mean, wave) / (float)a.cols;
-      // past the row's end v is 0 and stays it
+      // past the row's end v is 0 and stays 0
       auto inside = [&](int j) { return (t + j * C::kRowThreads) * E < a.cols; };
       float sd[NV];
 #pragma unroll
